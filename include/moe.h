@@ -52,7 +52,9 @@ typedef enum {
 typedef enum {
     MOE_F32 = 0,               /* IEEE binary32 */
     MOE_BF16 = 1,              /* bfloat16 */
-    MOE_FP8_E4M3 = 2           /* OCP 8-bit E4M3 ("FN": max 448, no infinities), weights only */
+    MOE_FP8_E4M3 = 2,          /* OCP 8-bit E4M3 ("FN": max 448, no infinities), weights only */
+    MOE_MXFP4 = 3,             /* OCP microscaled E2M1: two codes to a byte, an E8M0 scale per 32 elements */
+    MOE_MXFP8 = 4              /* OCP microscaled E4M3: an E8M0 scale per 32 elements (moe_quantize_mx only) */
 } moe_dtype_t;
 
 /*
@@ -187,6 +189,32 @@ moe_status_t moe_route_limited(const moe_shape_t* shape, const void* x, const fl
  */
 moe_status_t moe_quantize_e4m3(int64_t rows, int64_t cols, const void* x, uint8_t* q, float* scales,
                                hipStream_t stream);
+
+/*
+ * Quantisation to a microscaled format (OCP MX): every group of 32 consecutive columns of a row shares one
+ * E8M0 scale, a byte c standing for 2^(c - 127).  With a the group's largest magnitude,
+ * c - 127 = floor(log2 a) - emax clamped to [-127, 127] (emax 2 for MXFP4, 8 for MXFP8; a = 0: c = 0), and an
+ * element is v / 2^(c - 127) rounded to the nearest value of its type, ties to even, saturated to +-6 (E2M1)
+ * or +-448 (E4M3).  A group that holds an infinity or NaN gets c = 255 (NaN) and zero codes.
+ *   x       [rows, cols] x_dtype (MOE_BF16 or MOE_F32), 16-byte aligned
+ *   format  MOE_MXFP4 or MOE_MXFP8
+ *   q       MXFP4: [rows, cols / 2] bytes, column 2i in the low half of byte i, column 2i + 1 in the high half;
+ *           MXFP8: [rows, cols] E4M3 codes.  16-byte aligned (written)
+ *   scales  [rows, cols / 32] E8M0 bytes (written)
+ * cols not a multiple of 32, rows * cols above 2^34, other dtypes and formats: MOE_ERR_UNSUPPORTED; rows < 0 or
+ * cols <= 0: MOE_ERR_INVALID_ARG.
+ * rows = 0: a no-op.  Null or misaligned pointers return MOE_ERR_INVALID_ARG before any launch.
+ */
+moe_status_t moe_quantize_mx(int64_t rows, int64_t cols, const void* x, int32_t x_dtype, int32_t format, uint8_t* q,
+                             uint8_t* scales, hipStream_t stream);
+
+/*
+ * The values of a microscaled matrix: code * 2^(c - 127) as fp32 or bf16 (both exact, but that bf16 rounds
+ * MXFP8 values under 2^-133; NaN where c = 255 or an E4M3 code is NaN).  Layouts, limits and errors as
+ * moe_quantize_mx; out [rows, cols] out_dtype (MOE_BF16 or MOE_F32), 16-byte aligned.
+ */
+moe_status_t moe_dequantize_mx(int64_t rows, int64_t cols, const uint8_t* q, const uint8_t* scales, int32_t format,
+                               int32_t out_dtype, void* out, hipStream_t stream);
 
 /*
  * Group-limited routing ("Technical Architecture and Core Innovations", "Architectural Breakthroughs",

@@ -11,12 +11,12 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
-MOE_F32, MOE_BF16, MOE_FP8_E4M3 = 0, 1, 2
+MOE_F32, MOE_BF16, MOE_FP8_E4M3, MOE_MXFP4, MOE_MXFP8 = 0, 1, 2, 3, 4
 STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "MOE_ERR_WORKSPACE", 4: "MOE_ERR_HIP",
           5: "MOE_ERR_SCRATCH"}
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_forward", "moe_forward_staged", "moe_route_limited",
            "moe_route_grouped", "moe_forward_shard", "moe_expert_utilization", "moe_forward_noalloc",
-           "moe_quantize_e4m3", "moe_status_string")
+           "moe_quantize_e4m3", "moe_quantize_mx", "moe_dequantize_mx", "moe_status_string")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 NUM_STAGES = 7
 STAGE_NAMES = ("router_logits", "topk_softmax", "permute", "x_quant", "up_gemm", "down_gemm", "combine")
@@ -60,6 +60,11 @@ def lib() -> ctypes.CDLL:
         L.moe_route_grouped.argtypes = [sp, i64] + [vp] * 10 + [ctypes.c_size_t, vp]
         L.moe_quantize_e4m3.restype = ctypes.c_int
         L.moe_quantize_e4m3.argtypes = [i64, i64, vp, vp, vp, vp]
+        i32 = ctypes.c_int32
+        L.moe_quantize_mx.restype = ctypes.c_int
+        L.moe_quantize_mx.argtypes = [i64, i64, vp, i32, i32, vp, vp, vp]
+        L.moe_dequantize_mx.restype = ctypes.c_int
+        L.moe_dequantize_mx.argtypes = [i64, i64, vp, vp, i32, i32, vp, vp]
         L.moe_forward_shard.restype = ctypes.c_int
         L.moe_forward_shard.argtypes = [sp] + [vp] * 4 + [i64] * 3 + [vp] * 17 + [ctypes.c_size_t, vp, vp]
         L.moe_expert_utilization.restype = ctypes.c_int
@@ -159,6 +164,42 @@ def moe_quantize_e4m3(x):
     if st:
         raise MoeError(st, "moe_quantize_e4m3")
     return q, s
+
+
+def moe_quantize_mx(x, fmt):
+    """Quantise a bf16 or fp32 [rows, cols] device tensor to MOE_MXFP4 or MOE_MXFP8: (codes, scales), uint8.
+
+    Codes [rows, cols / 2] (MXFP4, two to a byte, the lower column in the low half) or [rows, cols] (MXFP8:
+    E4M3); scales [rows, cols / 32], E8M0 bytes."""
+    if x.dtype not in (torch.bfloat16, torch.float32) or x.dim() != 2 or not x.is_contiguous():
+        raise ValueError("x must be a contiguous 2-D bf16 or fp32 tensor")
+    rows, cols = x.shape
+    q = torch.empty((rows, cols // 2 if fmt == MOE_MXFP4 else cols), dtype=torch.uint8, device=x.device)
+    s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
+    with torch.cuda.device(x.device):
+        st = lib().moe_quantize_mx(rows, cols, _ptr(x), _act_code(x), fmt, _ptr(q), _ptr(s), _stream(x.device))
+    if st:
+        raise MoeError(st, "moe_quantize_mx")
+    return q, s
+
+
+def moe_dequantize_mx(q, scales, fmt, dtype=torch.bfloat16):
+    """The values [rows, cols] (bf16 or fp32) of what moe_quantize_mx returned for format `fmt`."""
+    rows, cols = scales.shape[0], scales.shape[-1] * 32
+    if q.shape != (rows, cols // 2 if fmt == MOE_MXFP4 else cols) or scales.dim() != 2:
+        raise ValueError("codes and scales do not have the shapes of one matrix")
+    if q.element_size() != 1 or scales.element_size() != 1 or not q.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("codes and scales must be contiguous byte tensors")
+    if q.device != scales.device:
+        raise ValueError("codes and scales must be on one device")
+    if dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("dtype must be bf16 or fp32")
+    out = torch.empty((rows, cols), dtype=dtype, device=q.device)
+    with torch.cuda.device(q.device):
+        st = lib().moe_dequantize_mx(rows, cols, _ptr(q), _ptr(scales), fmt, _act_code(out), _ptr(out), _stream(q.device))
+    if st:
+        raise MoeError(st, "moe_dequantize_mx")
+    return out
 
 
 def moe_route_grouped(x, Wg, bias, k, n_group, workspace=None):

@@ -314,6 +314,38 @@ extern "C" moe_status_t moe_quantize_e4m3(int64_t rows, int64_t cols, const void
     return MOE_OK;
 }
 
+// Host-side checks of the microscaled conversions.
+static moe_status_t check_mx(int64_t rows, int64_t cols, int32_t dtype, int32_t format, const void* wide,
+                             const void* q, const void* scales)
+{
+    if (rows < 0 || cols <= 0) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_F32) return MOE_ERR_UNSUPPORTED;
+    if (format != MOE_MXFP4 && format != MOE_MXFP8) return MOE_ERR_UNSUPPORTED;
+    // a thread per eight elements: a launch holds fewer than 2^32 threads
+    if (cols % 32 || cols > ((int64_t)1 << 34) || rows > ((int64_t)1 << 34) / cols) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!wide || !q || !scales || !aligned16(wide) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+extern "C" moe_status_t moe_quantize_mx(int64_t rows, int64_t cols, const void* x, int32_t x_dtype, int32_t format,
+                                        uint8_t* q, uint8_t* scales, hipStream_t stream)
+{
+    const moe_status_t st = check_mx(rows, cols, x_dtype, format, x, q, scales);
+    if (st != MOE_OK || rows == 0) return st;
+    MOE_TRY(launch_quantize_mx(rows * cols, format == MOE_MXFP4, x_dtype == MOE_BF16, x, q, scales, stream));
+    return MOE_OK;
+}
+
+extern "C" moe_status_t moe_dequantize_mx(int64_t rows, int64_t cols, const uint8_t* q, const uint8_t* scales,
+                                          int32_t format, int32_t out_dtype, void* out, hipStream_t stream)
+{
+    const moe_status_t st = check_mx(rows, cols, out_dtype, format, out, q, scales);
+    if (st != MOE_OK || rows == 0) return st;
+    MOE_TRY(launch_dequantize_mx(rows * cols, format == MOE_MXFP4, out_dtype == MOE_BF16, q, scales, out, stream));
+    return MOE_OK;
+}
+
 extern "C" moe_status_t moe_expert_utilization(int64_t E, const int32_t* counts, float* util, int32_t* flags,
                                                int32_t* summary, hipStream_t stream)
 {

@@ -193,6 +193,11 @@ hipError_t launch_combine_partial(const moe_shape_t& s, const int32_t* idx, cons
                                   hipStream_t stream);
 hipError_t launch_expert_utilization(int E, const int32_t* counts, float* util, int32_t* flags, int32_t* summary,
                                      hipStream_t stream);
+// n elements (a multiple of 32) to or from a microscaled format; bf16: the other side is bf16, else fp32.
+hipError_t launch_quantize_mx(int64_t n, bool fp4, bool bf16, const void* x, uint8_t* q, uint8_t* scales,
+                              hipStream_t stream);
+hipError_t launch_dequantize_mx(int64_t n, bool fp4, bool bf16, const uint8_t* q, const uint8_t* scales, void* out,
+                                hipStream_t stream);
 hipError_t launch_combine(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
                           hipStream_t stream);
 
