@@ -25,7 +25,8 @@
  *  - Calls are reentrant.  Concurrent calls must use different workspaces and outputs.
  *  - fp8 weights are quantised in 128 x 128 blocks and fp8 activations in 1 x 128 groups: the block
  *    edge is fixed at 128 (the configurations' quantisation block), so d, inter and inter_shared are
- *    multiples of 128 for every dtype.
+ *    multiples of 128 for every dtype.  MXFP4 weights and the activations that meet them (as MXFP8) carry
+ *    one power-of-two scale per 32 elements along the reduction.
  *  - Inputs are assumed finite; NaN/Inf inputs are outside the contract.
  */
 #ifndef MOE_H
@@ -67,7 +68,7 @@ typedef enum {
  *   inter_shared  shared expert width (n_shared * inter = 2048), multiple of 128
  *   act_dtype     dtype of x, y and every activation between linears: MOE_F32 or MOE_BF16
  *   w_dtype       dtype of W1, W3, W2 and S1, S3, S2.  Supported pairs (act, w):
- *                 (F32, F32), (BF16, BF16), (BF16, FP8_E4M3).
+ *                 (F32, F32), (BF16, BF16), (BF16, FP8_E4M3), (BF16, MXFP4).
  * The router is fp32 in every case (Wg, bias and logits).
  */
 typedef struct {
@@ -121,19 +122,22 @@ moe_status_t moe_route(const moe_shape_t* shape, const void* x, const float* Wg,
  *   S1, S3   [inter_shared, d] w_dtype;  S2 [d, inter_shared] w_dtype
  *   W1s, W3s [E, inter/128, d/128] fp32, W2s [E, d/128, inter/128] fp32, S1s, S3s
  *            [inter_shared/128, d/128] fp32, S2s [d/128, inter_shared/128] fp32: one scale per 128x128
- *            weight block, value = code * scale.  Required iff w_dtype == MOE_FP8_E4M3, else ignored.
+ *            weight block, value = code * scale.  Required iff w_dtype == MOE_FP8_E4M3 or MOE_MXFP4, else ignored.
+ *            MOE_MXFP4: the weights are [.., out, in / 2] bytes and the scales [.., out, in / 32] E8M0 bytes (4-byte
+ *            aligned), as moe_quantize_mx writes them for the [out, in] matrix.
  *   y    out [T, d] act_dtype
  *   idx_out, w_out [T, k], counts_out [E]: optional copies of the routing (NULL to skip)
  * Rounding: each linear's output is rounded to act_dtype; silu(g)*u is formed in fp32 and rounded to
  * act_dtype; with fp8 weights, x and h are quantised per 1x128 group (s = amax/448, codes = E4M3
- * round-to-nearest-even of v/s); the combine accumulates w * expert output and the shared output in
+ * round-to-nearest-even of v/s), with MXFP4 weights per 1x32 group to MXFP8 by moe_quantize_mx's rule; the
+ * combine accumulates w * expert output and the shared output in
  * fp32 in a fixed order and rounds once to act_dtype.  The result is bitwise deterministic.
  */
 moe_status_t moe_forward(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
                          const void* W1, const void* W3, const void* W2,
-                         const float* W1s, const float* W3s, const float* W2s,
+                         const void* W1s, const void* W3s, const void* W2s,
                          const void* S1, const void* S3, const void* S2,
-                         const float* S1s, const float* S3s, const float* S2s,
+                         const void* S1s, const void* S3s, const void* S2s,
                          void* y, int32_t* idx_out, float* w_out, int32_t* counts_out,
                          void* workspace, size_t workspace_bytes, hipStream_t stream);
 
@@ -150,9 +154,9 @@ moe_status_t moe_forward(const moe_shape_t* shape, const void* x, const float* W
 #define MOE_NUM_STAGES 7
 moe_status_t moe_forward_staged(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
                                 const void* W1, const void* W3, const void* W2,
-                                const float* W1s, const float* W3s, const float* W2s,
+                                const void* W1s, const void* W3s, const void* W2s,
                                 const void* S1, const void* S3, const void* S2,
-                                const float* S1s, const float* S3s, const float* S2s,
+                                const void* S1s, const void* S3s, const void* S2s,
                                 void* y, int32_t* idx_out, float* w_out, int32_t* counts_out,
                                 void* workspace, size_t workspace_bytes, hipStream_t stream,
                                 hipEvent_t* events);
@@ -173,6 +177,26 @@ moe_status_t moe_route_limited(const moe_shape_t* shape, const void* x, const fl
                                const uint8_t* allowed, int32_t* idx, float* w, int32_t* counts, int32_t* offsets,
                                int32_t* sorted_slots, int32_t* pos, void* workspace, size_t workspace_bytes,
                                hipStream_t stream);
+
+/*
+ * The layer for a routing that the caller brings (from moe_route_grouped or moe_route_limited, a router of its own,
+ * or one with a capacity): moe_forward without its gate.
+ *   idx      [T, k] int32: slot j of token t goes to expert idx[t][j].  An entry outside [0, E) (-1 by custom) is
+ *            a slot without an expert: it adds nothing, whatever its weight holds.  A token may have no expert at
+ *            all (its y is the shared expert's output) and may name an expert twice (both weights count).
+ *   w        [T, k] fp32 weights, used as they are (not normalised)
+ *   counts_out [E] int32 rows per expert (a token that names an expert twice is one row), or NULL
+ * y[t] = sum_j w[t][j] * SwiGLU_{idx[t][j]}(x[t]) + SwiGLU_shared(x[t]), the sum over j by ascending expert.
+ * All other arguments, roundings, guarantees and errors as moe_forward; moe_workspace_size applies.  With the idx
+ * and w that moe_forward reports, y is moe_forward's bit for bit.
+ */
+moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const int32_t* idx, const float* w,
+                                const void* W1, const void* W3, const void* W2,
+                                const void* W1s, const void* W3s, const void* W2s,
+                                const void* S1, const void* S3, const void* S2,
+                                const void* S1s, const void* S3s, const void* S2s,
+                                void* y, int32_t* counts_out, void* workspace, size_t workspace_bytes,
+                                hipStream_t stream);
 
 /*
  * fp8 activation quantisation, the layer's step for activations entering an fp8 linear (the fp8
@@ -262,9 +286,9 @@ moe_status_t moe_route_grouped(const moe_shape_t* shape, int64_t n_group, const 
 moe_status_t moe_forward_shard(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
                                const uint8_t* allowed, int64_t e0, int64_t e1, int64_t n_shared,
                                const void* W1, const void* W3, const void* W2,
-                               const float* W1s, const float* W3s, const float* W2s,
+                               const void* W1s, const void* W3s, const void* W2s,
                                const void* S1, const void* S3, const void* S2,
-                               const float* S1s, const float* S3s, const float* S2s,
+                               const void* S1s, const void* S3s, const void* S2s,
                                float* y_partial, int32_t* idx_out, float* w_out, int32_t* counts_out,
                                void* workspace, size_t workspace_bytes, hipStream_t stream, hipEvent_t* events);
 
@@ -303,9 +327,9 @@ moe_status_t moe_expert_utilization(int64_t E, const int32_t* counts, float* uti
 #define MOE_NOALLOC_SCRATCH_BYTES ((size_t)64 << 20)
 moe_status_t moe_forward_noalloc(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
                                  const void* W1, const void* W3, const void* W2,
-                                 const float* W1s, const float* W3s, const float* W2s,
+                                 const void* W1s, const void* W3s, const void* W2s,
                                  const void* S1, const void* S3, const void* S2,
-                                 const float* S1s, const float* S3s, const float* S2s,
+                                 const void* S1s, const void* S3s, const void* S2s,
                                  void* y, int32_t* idx_out, float* w_out, int32_t* counts_out,
                                  hipStream_t stream);
 

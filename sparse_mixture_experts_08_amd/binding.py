@@ -16,7 +16,7 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
           5: "MOE_ERR_SCRATCH"}
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_forward", "moe_forward_staged", "moe_route_limited",
            "moe_route_grouped", "moe_forward_shard", "moe_expert_utilization", "moe_forward_noalloc",
-           "moe_quantize_e4m3", "moe_quantize_mx", "moe_dequantize_mx", "moe_status_string")
+           "moe_quantize_e4m3", "moe_quantize_mx", "moe_dequantize_mx", "moe_forward_routed", "moe_status_string")
 NOALLOC_SCRATCH_BYTES = 64 << 20
 NUM_STAGES = 7
 STAGE_NAMES = ("router_logits", "topk_softmax", "permute", "x_quant", "up_gemm", "down_gemm", "combine")
@@ -67,6 +67,8 @@ def lib() -> ctypes.CDLL:
         L.moe_dequantize_mx.argtypes = [i64, i64, vp, vp, i32, i32, vp, vp]
         L.moe_forward_shard.restype = ctypes.c_int
         L.moe_forward_shard.argtypes = [sp] + [vp] * 4 + [i64] * 3 + [vp] * 17 + [ctypes.c_size_t, vp, vp]
+        L.moe_forward_routed.restype = ctypes.c_int
+        L.moe_forward_routed.argtypes = [sp] + [vp] * 18 + [ctypes.c_size_t, vp]
         L.moe_expert_utilization.restype = ctypes.c_int
         L.moe_expert_utilization.argtypes = [i64] + [vp] * 5
         L.moe_forward_noalloc.restype = ctypes.c_int
@@ -85,7 +87,10 @@ def _act_code(t: torch.Tensor) -> int:
     return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}.get(t.dtype, -1)
 
 
-def _w_code(t: torch.Tensor) -> int:
+def _w_code(t: torch.Tensor, cols=None) -> int:
+    """Weight type of a stored matrix [.., out, in]; byte tensors of half the `cols` input features hold MXFP4."""
+    if cols is not None and t.element_size() == 1 and t.shape[-1] * 2 == cols:
+        return MOE_MXFP4
     return {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_FP8_E4M3,
             torch.float8_e4m3fn: MOE_FP8_E4M3}.get(t.dtype, -1)
 
@@ -214,7 +219,8 @@ def _check_allowed(allowed, E):
 
 def moe_forward(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, workspace=None, routing=False,
                 events=None):
-    """Layer output y [T, d] (x's dtype).  `scales`: dict of W1s, W3s, W2s, S1s, S3s, S2s for fp8 weights.
+    """Layer output y [T, d] (x's dtype).  `scales`: dict of W1s, W3s, W2s, S1s, S3s, S2s for fp8
+    (fp32 block scales) and MXFP4 weights (E8M0 bytes; the weights [.., out, in / 2] bytes).
 
     With routing=True returns (y, dict(idx, w, counts)).  With `events` (a ctypes array of
     NUM_STAGES + 1 hipEvent_t handles) calls moe_forward_staged, which records them between stages.
@@ -222,7 +228,7 @@ def moe_forward(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, wor
     T, d = x.shape
     E, inter = W1.shape[0], W1.shape[1]
     inter_s = S1.shape[0]
-    shape = make_shape(T, d, E, k, inter, inter_s, _act_code(x), _w_code(W1))
+    shape = make_shape(T, d, E, k, inter, inter_s, _act_code(x), _w_code(W1, d))
     dev = x.device
     workspace, need = _workspace(shape, dev, workspace)
     if y is None:
@@ -247,12 +253,77 @@ def moe_forward(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, wor
     return (y, r) if routing else y
 
 
+_SCALES = ("W1s", "W3s", "W2s", "S1s", "S3s", "S2s")
+
+
+def _layer(x, k, E, W1, W3, W2, S1, S3, S2, scales, y, vectors):
+    """Checks one layer call's tensors; returns (shape, scales, y).  `vectors`: (name, tensor or None, dtype, shape)
+    of the call's other inputs."""
+    if x.dim() != 2 or x.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError("x must be a 2-D bf16 or fp32 tensor")
+    T, d = x.shape
+    if W1.dim() != 3 or S1.dim() != 2:
+        raise ValueError("W1 must be [E, inter, d], S1 [inter_shared, d]")
+    inter, inter_s = W1.shape[1], S1.shape[0]
+    w = _w_code(W1, d)
+    half = 2 if w == MOE_MXFP4 else 1
+    sc = dict(scales or {})
+    want = [("W1", W1, (E, inter, d // half)), ("W3", W3, (E, inter, d // half)), ("W2", W2, (E, d, inter // half)),
+            ("S1", S1, (inter_s, d // half)), ("S3", S3, (inter_s, d // half)), ("S2", S2, (d, inter_s // half))]
+    tensors = [("x", x, None)]
+    for name, t, size in want:
+        if t.shape != size or _w_code(t, size[-1] * half) != w:
+            raise ValueError(f"{name} must be {list(size)} with W1's type")
+        tensors.append((name, t, None))
+        if w in (MOE_FP8_E4M3, MOE_MXFP4):
+            s = sc.get(name + "s")
+            ssize = size[:-2] + ((size[-2], size[-1] * half // 32) if half == 2 else (size[-2] // 128, size[-1] // 128))
+            if s is None or s.shape != ssize or s.element_size() != (1 if half == 2 else 4):
+                raise ValueError(f"scales[{name}s] must be {list(ssize)} {'E8M0 bytes' if half == 2 else 'fp32'}")
+            tensors.append((name + "s", s, None))
+    for name, t, dtype, size in vectors:
+        if t is not None and (t.dtype != dtype or t.shape != size):
+            raise ValueError(f"{name} must be {list(size)} {dtype}")
+        tensors.append((name, t, None))
+    if y is None:
+        y = torch.empty_like(x, memory_format=torch.contiguous_format)
+    elif y.shape != x.shape or y.dtype != x.dtype:
+        raise ValueError("y must have x's shape and type")
+    for name, t, _ in tensors + [("y", y, None)]:
+        if t is not None and (not t.is_contiguous() or t.device != x.device):
+            raise ValueError(f"{name} must be contiguous and on x's device")
+    return make_shape(T, d, E, k, inter, inter_s, _act_code(x), w), sc, y
+
+
+def moe_forward_routed(x, idx, w, W1, W3, W2, S1, S3, S2, scales=None, y=None, workspace=None, counts=False):
+    """The layer for a given routing: idx int32 [T, k] (an entry outside [0, E) is a slot without an expert), w fp32
+    [T, k].  Weights and `scales` as moe_forward.  With counts=True returns (y, counts int32 [E])."""
+    if idx.dim() != 2:
+        raise ValueError("idx must be [T, k]")
+    k, E = idx.shape[1], W1.shape[0]
+    shape, sc, y = _layer(x, k, E, W1, W3, W2, S1, S3, S2, scales, y,
+                          [("idx", idx, torch.int32, (x.shape[0], k)), ("w", w, torch.float32, (x.shape[0], k))])
+    dev = x.device
+    with torch.cuda.device(dev):
+        workspace, need = _workspace(shape, dev, workspace)
+        c = torch.empty(E, dtype=torch.int32, device=dev) if counts else None
+        if counts and x.shape[0] == 0:
+            c.zero_()                                  # no tokens: the library writes nothing
+        st = lib().moe_forward_routed(ctypes.byref(shape), _ptr(x), _ptr(idx), _ptr(w), _ptr(W1), _ptr(W3), _ptr(W2),
+                                      *[_ptr(sc.get(n)) for n in _SCALES[:3]], _ptr(S1), _ptr(S3), _ptr(S2),
+                                      *[_ptr(sc.get(n)) for n in _SCALES[3:]], _ptr(y), _ptr(c), _ptr(workspace),
+                                      workspace.numel(), _stream(dev))
+    if st:
+        raise MoeError(st, "moe_forward_routed")
+    return (y, c) if counts else y
+
+
 def moe_forward_noalloc(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, routing=False):
     """moe_forward_noalloc: moe_forward with the library's static device scratch as its workspace (nothing is
     allocated by the call itself; y and the routing copies are allocated here unless given)."""
     T, d = x.shape
     E, inter = W1.shape[0], W1.shape[1]
-    shape = make_shape(T, d, E, k, inter, S1.shape[0], _act_code(x), _w_code(W1))
+    shape = make_shape(T, d, E, k, inter, S1.shape[0], _act_code(x), _w_code(W1, d))
     dev = x.device
     if y is None:
         y = torch.empty_like(x)
@@ -300,7 +371,7 @@ def moe_forward_shard(x, Wg, bias, k, e0, e1, W1, W3, W2, S1, S3, S2, inter, int
     E = Wg.shape[0]
     n_shared = 0 if S1 is None else S1.shape[0]
     wt = W1 if W1 is not None else S1
-    shape = make_shape(T, d, E, k, inter, inter_shared, _act_code(x), _w_code(wt) if wt is not None else _act_code(x))
+    shape = make_shape(T, d, E, k, inter, inter_shared, _act_code(x), _w_code(wt, d) if wt is not None else _act_code(x))
     dev = x.device
     workspace, need = _workspace(shape, dev, workspace)
     if y_partial is None:
@@ -328,16 +399,21 @@ def moe_forward_shard(x, Wg, bias, k, e0, e1, W1, W3, W2, S1, S3, S2, inter, int
 def shard_weights(inp: dict, e0: int, e1: int, s0: int, s1: int) -> dict:
     """The rank-local weight arrays of experts [e0, e1) and shared features [s0, s1) of a full-layer dict
     (as workloads.generate makes), stored densely as moe_forward_shard expects."""
-    fp8 = inp.get("W1s") is not None
+    scaled = inp.get("W1s") is not None
+    half = 2 if inp["S2"].shape[1] * 2 == inp["S1"].shape[0] else 1          # MXFP4: two codes to a byte
     out = {}
     if e1 > e0:
-        for n in ("W1", "W3", "W2") + (("W1s", "W3s", "W2s") if fp8 else ()):
+        for n in ("W1", "W3", "W2") + (("W1s", "W3s", "W2s") if scaled else ()):
             out[n] = inp[n][e0:e1].contiguous()
     if s1 > s0:
         out["S1"] = inp["S1"][s0:s1].contiguous()
         out["S3"] = inp["S3"][s0:s1].contiguous()
-        out["S2"] = inp["S2"][:, s0:s1].contiguous()
-        if fp8:
+        out["S2"] = inp["S2"][:, s0 // half:s1 // half].contiguous()
+        if half == 2:
+            out["S1s"] = inp["S1s"][s0:s1].contiguous()
+            out["S3s"] = inp["S3s"][s0:s1].contiguous()
+            out["S2s"] = inp["S2s"][:, s0 // 32:s1 // 32].contiguous()
+        elif scaled:
             out["S1s"] = inp["S1s"][s0 // 128:s1 // 128].contiguous()
             out["S3s"] = inp["S3s"][s0 // 128:s1 // 128].contiguous()
             out["S2s"] = inp["S2s"][:, s0 // 128:s1 // 128].contiguous()

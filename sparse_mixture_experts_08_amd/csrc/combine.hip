@@ -11,8 +11,9 @@
 namespace moe {
 
 // K > 0: k fixed at compile time, so the slot sort is a register-only network and the k + 1 row loads of a
-// vector are all in flight together; K = 0: any k <= 16, one row load at a time.
-template <bool ACT_BF16, int K>
+// vector are all in flight together; K = 0: any k <= 16, one row load at a time.  GIVEN: a pos of -1 is a slot
+// without an expert; such slots sort first, load row 0 (which may hold anything) and are not added.
+template <bool ACT_BF16, int K, bool GIVEN>
 __global__ __launch_bounds__(512) void combine_kernel(const int32_t* __restrict__ pos, const float* __restrict__ w,
                                                       const uint8_t* __restrict__ y_rows, int T, int d, int k_rt,
                                                       uint8_t* __restrict__ y)
@@ -91,7 +92,8 @@ __global__ __launch_bounds__(512) void combine_kernel(const int32_t* __restrict_
         // current vector again, with no branch around the loads).
         auto load = [&](uint4 (&rows)[K + 1], int cc) {
 #pragma unroll
-            for (int j = 0; j < K; j++) rows[j] = *(const uint4*)(y_rows + ((int64_t)rr[j] * d + cc) * EB);
+            for (int j = 0; j < K; j++)
+                rows[j] = *(const uint4*)(y_rows + ((int64_t)(GIVEN ? max(rr[j], 0) : rr[j]) * d + cc) * EB);
             rows[K] = *(const uint4*)(y_rows + (shared_row * d + cc) * EB);
         };
         if (c >= d) return;
@@ -104,7 +106,8 @@ __global__ __launch_bounds__(512) void combine_kernel(const int32_t* __restrict_
 #pragma unroll
             for (int e = 0; e < VE; e++) acc[e] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < K; j++) add_row(acc, cur[j], ww[j]);
+            for (int j = 0; j < K; j++)
+                if (!GIVEN || rr[j] >= 0) add_row(acc, cur[j], ww[j]);
             finish(acc, cur[K], c);
 #pragma unroll
             for (int j = 0; j <= K; j++) cur[j] = nxt[j];
@@ -114,7 +117,10 @@ __global__ __launch_bounds__(512) void combine_kernel(const int32_t* __restrict_
             float acc[VE];
 #pragma unroll
             for (int e = 0; e < VE; e++) acc[e] = 0.0f;
-            for (int j = 0; j < k; j++) add_row(acc, *(const uint4*)(y_rows + ((int64_t)rr[j] * d + c) * EB), ww[j]);
+            for (int j = 0; j < k; j++) {
+                if (GIVEN && rr[j] < 0) continue;
+                add_row(acc, *(const uint4*)(y_rows + ((int64_t)rr[j] * d + c) * EB), ww[j]);
+            }
             finish(acc, *(const uint4*)(y_rows + (shared_row * d + c) * EB), c);
         }
     }
@@ -134,7 +140,7 @@ static dim3 combine_grid(const moe_shape_t& s, int threads)
     return dim3((unsigned)s.T, s.T >= 1024 ? 1u : (unsigned)((s.d + chunk - 1) / chunk));
 }
 
-template <bool ACT_BF16>
+template <bool ACT_BF16, bool GIVEN>
 static void launch_combine_t(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
                              hipStream_t stream)
 {
@@ -144,18 +150,26 @@ static void launch_combine_t(const moe_shape_t& s, const int32_t* pos, const flo
     const uint8_t* rows = (const uint8_t*)ws.y_rows;
     uint8_t* out = (uint8_t*)y;
     switch (k) {
-    case 4: combine_kernel<ACT_BF16, 4><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
-    case 6: combine_kernel<ACT_BF16, 6><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
-    case 8: combine_kernel<ACT_BF16, 8><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
-    default: combine_kernel<ACT_BF16, 0><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
+    case 4: combine_kernel<ACT_BF16, 4, GIVEN><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
+    case 6: combine_kernel<ACT_BF16, 6, GIVEN><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
+    case 8: combine_kernel<ACT_BF16, 8, GIVEN><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
+    default: combine_kernel<ACT_BF16, 0, GIVEN><<<grid, nt, 0, stream>>>(pos, w, rows, T, d, k, out); break;
     }
 }
 
 hipError_t launch_combine(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
                           hipStream_t stream)
 {
-    if (s.act_dtype == MOE_BF16) launch_combine_t<true>(s, pos, w, ws, y, stream);
-    else launch_combine_t<false>(s, pos, w, ws, y, stream);
+    if (s.act_dtype == MOE_BF16) launch_combine_t<true, false>(s, pos, w, ws, y, stream);
+    else launch_combine_t<false, false>(s, pos, w, ws, y, stream);
+    return hipGetLastError();
+}
+
+hipError_t launch_combine_given(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
+                                hipStream_t stream)
+{
+    if (s.act_dtype == MOE_BF16) launch_combine_t<true, true>(s, pos, w, ws, y, stream);
+    else launch_combine_t<false, true>(s, pos, w, ws, y, stream);
     return hipGetLastError();
 }
 

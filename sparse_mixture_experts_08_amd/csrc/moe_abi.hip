@@ -17,10 +17,10 @@ int tile_rows(const moe_shape_t& s)
     // streaming).  Otherwise bf16 takes 256-row tiles: an expert of up to 256 rows reads its weights once,
     // and a 256 x 256 output block needs fewer staged bytes per MFMA than 128 x 512; row blocks past a
     // tile's end are skipped.  fp8 takes 256-row tiles above 192 rows per expert (fewer staged bytes and
-    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.
+    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.  MXFP4 as fp8.
     const int64_t per_expert = s.T * s.k / (s.E > 0 ? s.E : 1);
     if (per_expert <= 24) return 16;
-    if (s.w_dtype == MOE_FP8_E4M3) return per_expert > 192 ? 256 : 128;
+    if (s.w_dtype == MOE_FP8_E4M3 || s.w_dtype == MOE_MXFP4) return per_expert > 192 ? 256 : 128;
     if (s.act_dtype == MOE_F32) return 128;
     return 256;
 }
@@ -35,7 +35,7 @@ Workspace carve_workspace(const moe_shape_t& s, void* base)
     w.nchunks = (T + 63) / 64;
     w.max_tiles = rows / bm + E + 2;
     w.inter_max = s.inter > s.inter_shared ? s.inter : s.inter_shared;
-    const bool fp8 = s.w_dtype == MOE_FP8_E4M3;
+    const bool fp8 = s.w_dtype == MOE_FP8_E4M3, mx = s.w_dtype == MOE_MXFP4;
     const size_t act = s.act_dtype == MOE_F32 ? 4 : 2;
     size_t off = 0;
     char* b = (char*)base;
@@ -62,6 +62,11 @@ Workspace carve_workspace(const moe_shape_t& s, void* base)
         w.xs = (float*)take(sizeof(float) * T * (d / 128));
         w.h = take((size_t)rows * w.inter_max);
         w.hs = (float*)take(sizeof(float) * rows * (w.inter_max / 128));
+    } else if (mx) {
+        w.xq = (uint8_t*)take((size_t)T * d);
+        w.xe = (uint8_t*)take((size_t)T * (d / 32));
+        w.h = take((size_t)rows * w.inter_max);
+        w.he = (uint8_t*)take((size_t)rows * (w.inter_max / 32));
     } else {
         w.h = take(act * rows * w.inter_max);
     }
@@ -81,12 +86,13 @@ static moe_status_t check_shape(const moe_shape_t* s)
     if (s->d % 128 || s->inter % 128 || s->inter_shared % 128) return MOE_ERR_UNSUPPORTED;
     const bool ok = (s->act_dtype == MOE_F32 && s->w_dtype == MOE_F32) ||
                     (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_BF16) ||
-                    (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_FP8_E4M3);
+                    (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_FP8_E4M3) ||
+                    (s->act_dtype == MOE_BF16 && s->w_dtype == MOE_MXFP4);
     if (!ok) return MOE_ERR_UNSUPPORTED;
     // int32 indexing of rows and elements inside the kernels
     if (s->T > (1 << 24) || (s->T * (s->k + 1)) * s->d > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
     // 32-bit byte offsets inside the GEMM operands: x, h, and one expert's weights each under 4 GB
-    const int64_t ab = s->act_dtype == MOE_F32 ? 4 : 2, wb = s->w_dtype == MOE_FP8_E4M3 ? 1 : ab;
+    const int64_t ab = s->act_dtype == MOE_F32 ? 4 : 2, wb = s->w_dtype == MOE_FP8_E4M3 || s->w_dtype == MOE_MXFP4 ? 1 : ab;
     const int64_t inter_max = s->inter > s->inter_shared ? s->inter : s->inter_shared;
     const int64_t lim = (int64_t)1 << 32;
     if (s->T * s->d * ab >= lim || s->T * (s->k + 1) * inter_max * ab >= lim ||
@@ -188,9 +194,9 @@ extern "C" moe_status_t moe_route_limited(const moe_shape_t* shape, const void* 
 // Host-side checks of a layer call (everything but the workspace), shared by the entry points.
 static moe_status_t check_layer_args(const moe_shape_t* shape, const void* x, const float* Wg, int64_t e0, int64_t e1,
                                      int64_t n_shared, const void* W1, const void* W3, const void* W2,
-                                     const float* W1s, const float* W3s, const float* W2s, const void* S1,
-                                     const void* S3, const void* S2, const float* S1s, const float* S3s,
-                                     const float* S2s, const void* out)
+                                     const void* W1s, const void* W3s, const void* W2s, const void* S1,
+                                     const void* S3, const void* S2, const void* S1s, const void* S3s,
+                                     const void* S2s, const void* out)
 {
     moe_status_t st = check_shape(shape);
     if (st != MOE_OK) return st;
@@ -199,10 +205,14 @@ static moe_status_t check_layer_args(const moe_shape_t* shape, const void* x, co
     if (n_shared % 128) return MOE_ERR_UNSUPPORTED;
     if (s.T == 0) return MOE_OK;
     const bool routed = e1 > e0, with_shared = n_shared > 0;
-    const bool fp8 = s.w_dtype == MOE_FP8_E4M3;
+    const bool mx = s.w_dtype == MOE_MXFP4, scaled = s.w_dtype == MOE_FP8_E4M3 || mx;
     if (!x || !Wg || !out) return MOE_ERR_INVALID_ARG;
-    if (routed && (!W1 || !W3 || !W2 || (fp8 && (!W1s || !W3s || !W2s)))) return MOE_ERR_INVALID_ARG;
-    if (with_shared && (!S1 || !S3 || !S2 || (fp8 && (!S1s || !S3s || !S2s)))) return MOE_ERR_INVALID_ARG;
+    if (routed && (!W1 || !W3 || !W2 || (scaled && (!W1s || !W3s || !W2s)))) return MOE_ERR_INVALID_ARG;
+    if (with_shared && (!S1 || !S3 || !S2 || (scaled && (!S1s || !S3s || !S2s)))) return MOE_ERR_INVALID_ARG;
+    // MXFP4 scale bytes are read four at a time
+    for (const void* p : {routed && mx ? W1s : x, routed && mx ? W3s : x, routed && mx ? W2s : x,
+                          with_shared && mx ? S1s : x, with_shared && mx ? S3s : x, with_shared && mx ? S2s : x})
+        if ((uintptr_t)p & 3) return MOE_ERR_INVALID_ARG;
     if (x == out) return MOE_ERR_INVALID_ARG;
     const void* ptrs[] = {x, Wg, out, routed ? W1 : x, routed ? W3 : x, routed ? W2 : x, with_shared ? S1 : x,
                           with_shared ? S3 : x, with_shared ? S2 : x};
@@ -211,54 +221,75 @@ static moe_status_t check_layer_args(const moe_shape_t* shape, const void* x, co
     return MOE_OK;
 }
 
+// Routing that the caller brings instead of the gate's.
+struct GivenRouting {
+    const int32_t* idx;
+    const float* w;
+};
+
 // The layer or one expert-parallel rank's share of it.  Routed experts [e0, e1) (weights of expert e at
 // index e - e0 of W1/W3/W2), n_shared shared hidden features; y (act dtype, rounded) or y_partial (fp32).
+// given: the caller's routing (y only, the whole layer), else NULL and the gate's weight Wg.
 static moe_status_t layer_impl(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
                                const uint8_t* allowed, int64_t e0, int64_t e1, int64_t n_shared, const void* W1,
-                               const void* W3, const void* W2, const float* W1s, const float* W3s,
-                               const float* W2s, const void* S1, const void* S3, const void* S2, const float* S1s,
-                               const float* S3s, const float* S2s, void* y, float* y_partial, int32_t* idx_out,
+                               const void* W3, const void* W2, const void* W1s, const void* W3s,
+                               const void* W2s, const void* S1, const void* S3, const void* S2, const void* S1s,
+                               const void* S3s, const void* S2s, void* y, float* y_partial, int32_t* idx_out,
                                float* w_out, int32_t* counts_out, void* workspace, size_t workspace_bytes,
-                               hipStream_t stream, hipEvent_t* events)
+                               hipStream_t stream, hipEvent_t* events, const GivenRouting* given = nullptr)
 {
     void* out = y ? y : (void*)y_partial;
-    moe_status_t st = check_layer_args(shape, x, Wg, e0, e1, n_shared, W1, W3, W2, W1s, W3s, W2s, S1, S3, S2, S1s,
-                                       S3s, S2s, out);
+    // a given routing has no gate weight: x stands in for a pointer that passes the checks
+    moe_status_t st = check_layer_args(shape, x, given ? (const float*)x : Wg, e0, e1, n_shared, W1, W3, W2, W1s, W3s,
+                                       W2s, S1, S3, S2, S1s, S3s, S2s, out);
     if (st != MOE_OK) return st;
     const moe_shape_t& s = *shape;
     if (s.T == 0) return MOE_OK;
     const bool with_shared = n_shared > 0;
-    const bool fp8 = s.w_dtype == MOE_FP8_E4M3;
+    const bool fp8 = s.w_dtype == MOE_FP8_E4M3, mx = s.w_dtype == MOE_MXFP4;
     if (!workspace) return MOE_ERR_INVALID_ARG;
+    if (given && (!given->idx || !given->w || ((uintptr_t)given->idx & 3) || ((uintptr_t)given->w & 3)))
+        return MOE_ERR_INVALID_ARG;
     Workspace ws = carve_workspace(s, workspace);
     if (workspace_bytes < ws.total || ((uintptr_t)workspace & 255)) return MOE_ERR_WORKSPACE;
 
-    int32_t* idx = idx_out ? idx_out : ws.idx;
-    float* w = w_out ? w_out : ws.w;
+    const int32_t* idx = given ? given->idx : idx_out ? idx_out : ws.idx;
+    const float* w = given ? given->w : w_out ? w_out : ws.w;
     int32_t* counts = counts_out ? counts_out : ws.counts;
     const TileRange tr = {(int)e0, (int)e1, with_shared ? 1 : 0};
     const int bm = tile_rows(s);
     auto mark = [&](int i) -> hipError_t { return events ? hipEventRecord(events[i], stream) : hipSuccess; };
     MOE_TRY(mark(0));
-    MOE_TRY(launch_router_logits(s, x, Wg, bias, ws.logits, stream));
-    MOE_TRY(mark(1));
-    if (routing_is_fused(s)) {
-        MOE_TRY(launch_routing_fused(s, ws.logits, allowed, idx, w, counts, ws.offsets, ws.sorted_slots, ws.pos, ws, bm,
-                                     tr, stream));
+    if (given) {
+        MOE_TRY(mark(1));
         MOE_TRY(mark(2));
+        MOE_TRY(launch_permute_given(s, idx, counts, ws, bm, tr, stream));
     } else {
-        MOE_TRY(launch_topk(s, ws.logits, allowed, idx, w, ws, stream));
-        MOE_TRY(mark(2));
-        MOE_TRY(launch_permute(s, idx, counts, ws.offsets, ws.sorted_slots, ws.pos, ws, bm, tr, stream));
+        MOE_TRY(launch_router_logits(s, x, Wg, bias, ws.logits, stream));
+        MOE_TRY(mark(1));
+        if (routing_is_fused(s)) {
+            MOE_TRY(launch_routing_fused(s, ws.logits, allowed, (int32_t*)idx, (float*)w, counts, ws.offsets,
+                                         ws.sorted_slots, ws.pos, ws, bm, tr, stream));
+            MOE_TRY(mark(2));
+        } else {
+            MOE_TRY(launch_topk(s, ws.logits, allowed, (int32_t*)idx, (float*)w, ws, stream));
+            MOE_TRY(mark(2));
+            MOE_TRY(launch_permute(s, idx, counts, ws.offsets, ws.sorted_slots, ws.pos, ws, bm, tr, stream));
+        }
     }
     MOE_TRY(mark(3));
     if (fp8) MOE_TRY(launch_act_quant(s, x, ws, stream));
+    if (mx) MOE_TRY(launch_quantize_mx(s.T * s.d, false, true, x, ws.xq, ws.xe, stream));
     MOE_TRY(mark(4));
-    MOE_TRY(launch_up_gemm(s, x, W1, W3, W1s, W3s, S1, S3, S1s, S3s, ws, stream, (int)e0, (int)n_shared));
+    if (mx) MOE_TRY(launch_up_gemm_mx(s, W1, W3, W1s, W3s, S1, S3, S1s, S3s, ws, stream, (int)e0, (int)n_shared));
+    else MOE_TRY(launch_up_gemm(s, x, W1, W3, (const float*)W1s, (const float*)W3s, S1, S3, (const float*)S1s,
+                                (const float*)S3s, ws, stream, (int)e0, (int)n_shared));
     MOE_TRY(mark(5));
-    MOE_TRY(launch_down_gemm(s, W2, W2s, S2, S2s, ws, stream, (int)e0, (int)n_shared));
+    if (mx) MOE_TRY(launch_down_gemm_mx(s, W2, W2s, S2, S2s, ws, stream, (int)e0, (int)n_shared));
+    else MOE_TRY(launch_down_gemm(s, W2, (const float*)W2s, S2, (const float*)S2s, ws, stream, (int)e0, (int)n_shared));
     MOE_TRY(mark(6));
-    if (y) MOE_TRY(launch_combine(s, ws.pos, w, ws, y, stream));
+    if (given) MOE_TRY(launch_combine_given(s, ws.pos, w, ws, y, stream));
+    else if (y) MOE_TRY(launch_combine(s, ws.pos, w, ws, y, stream));
     else MOE_TRY(launch_combine_partial(s, idx, ws.pos, w, ws, (int)e0, (int)e1, with_shared, y_partial, stream));
     MOE_TRY(mark(7));
     return MOE_OK;
@@ -266,9 +297,9 @@ static moe_status_t layer_impl(const moe_shape_t* shape, const void* x, const fl
 
 extern "C" moe_status_t moe_forward_staged(const moe_shape_t* shape, const void* x, const float* Wg,
                                            const float* bias, const void* W1, const void* W3, const void* W2,
-                                           const float* W1s, const float* W3s, const float* W2s, const void* S1,
-                                           const void* S3, const void* S2, const float* S1s, const float* S3s,
-                                           const float* S2s, void* y, int32_t* idx_out, float* w_out,
+                                           const void* W1s, const void* W3s, const void* W2s, const void* S1,
+                                           const void* S3, const void* S2, const void* S1s, const void* S3s,
+                                           const void* S2s, void* y, int32_t* idx_out, float* w_out,
                                            int32_t* counts_out, void* workspace, size_t workspace_bytes,
                                            hipStream_t stream, hipEvent_t* events)
 {
@@ -279,9 +310,9 @@ extern "C" moe_status_t moe_forward_staged(const moe_shape_t* shape, const void*
 }
 
 extern "C" moe_status_t moe_forward(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
-                                    const void* W1, const void* W3, const void* W2, const float* W1s,
-                                    const float* W3s, const float* W2s, const void* S1, const void* S3,
-                                    const void* S2, const float* S1s, const float* S3s, const float* S2s, void* y,
+                                    const void* W1, const void* W3, const void* W2, const void* W1s,
+                                    const void* W3s, const void* W2s, const void* S1, const void* S3,
+                                    const void* S2, const void* S1s, const void* S3s, const void* S2s, void* y,
                                     int32_t* idx_out, float* w_out, int32_t* counts_out, void* workspace,
                                     size_t workspace_bytes, hipStream_t stream)
 {
@@ -292,15 +323,29 @@ extern "C" moe_status_t moe_forward(const moe_shape_t* shape, const void* x, con
 extern "C" moe_status_t moe_forward_shard(const moe_shape_t* shape, const void* x, const float* Wg,
                                           const float* bias, const uint8_t* allowed, int64_t e0, int64_t e1,
                                           int64_t n_shared, const void* W1, const void* W3, const void* W2,
-                                          const float* W1s, const float* W3s, const float* W2s, const void* S1,
-                                          const void* S3, const void* S2, const float* S1s, const float* S3s,
-                                          const float* S2s, float* y_partial, int32_t* idx_out, float* w_out,
+                                          const void* W1s, const void* W3s, const void* W2s, const void* S1,
+                                          const void* S3, const void* S2, const void* S1s, const void* S3s,
+                                          const void* S2s, float* y_partial, int32_t* idx_out, float* w_out,
                                           int32_t* counts_out, void* workspace, size_t workspace_bytes,
                                           hipStream_t stream, hipEvent_t* events)
 {
     return layer_impl(shape, x, Wg, bias, allowed, e0, e1, n_shared, W1, W3, W2, W1s, W3s, W2s, S1, S3, S2, S1s, S3s,
                       S2s, nullptr, y_partial, idx_out, w_out, counts_out, workspace, workspace_bytes, stream,
                       events);
+}
+
+extern "C" moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const int32_t* idx, const float* w,
+                                           const void* W1, const void* W3, const void* W2, const void* W1s,
+                                           const void* W3s, const void* W2s, const void* S1, const void* S3,
+                                           const void* S2, const void* S1s, const void* S3s, const void* S2s, void* y,
+                                           int32_t* counts_out, void* workspace, size_t workspace_bytes,
+                                           hipStream_t stream)
+{
+    if (!shape) return MOE_ERR_INVALID_ARG;
+    const GivenRouting given = {idx, w};
+    return layer_impl(shape, x, nullptr, nullptr, nullptr, 0, shape->E, shape->inter_shared, W1, W3, W2, W1s, W3s, W2s,
+                      S1, S3, S2, S1s, S3s, S2s, y, nullptr, nullptr, nullptr, counts_out, workspace, workspace_bytes,
+                      stream, nullptr, &given);
 }
 
 extern "C" moe_status_t moe_quantize_e4m3(int64_t rows, int64_t cols, const void* x, uint8_t* q, float* scales,
@@ -396,9 +441,9 @@ static void* scratch_on_current_device(hipError_t* err)
 
 extern "C" moe_status_t moe_forward_noalloc(const moe_shape_t* shape, const void* x, const float* Wg,
                                             const float* bias, const void* W1, const void* W3, const void* W2,
-                                            const float* W1s, const float* W3s, const float* W2s, const void* S1,
-                                            const void* S3, const void* S2, const float* S1s, const float* S3s,
-                                            const float* S2s, void* y, int32_t* idx_out, float* w_out,
+                                            const void* W1s, const void* W3s, const void* W2s, const void* S1,
+                                            const void* S3, const void* S2, const void* S1s, const void* S3s,
+                                            const void* S2s, void* y, int32_t* idx_out, float* w_out,
                                             int32_t* counts_out, hipStream_t stream)
 {
     if (!shape) return MOE_ERR_INVALID_ARG;

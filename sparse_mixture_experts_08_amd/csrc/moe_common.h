@@ -145,10 +145,12 @@ struct Workspace {
     int32_t* row_token;     // [T * k + T]  token of each expert-sorted row; shared rows last
     int4* tiles;            // [max_tiles]  (group, first row, rows, 0); group E is the shared expert
     int32_t* sync;          // [4]  sync[0]: number of tiles (written with the tile list)
-    uint8_t* xq;            // [T, d] E4M3 codes of x (fp8 weights only)
-    float* xs;              // [T, d / 128] their scales
-    void* h;                // [T * k + T, inter_max] act dtype, or E4M3 codes (fp8 weights)
+    uint8_t* xq;            // [T, d] E4M3 codes of x (fp8 and MXFP4 weights only)
+    float* xs;              // [T, d / 128] their scales (fp8)
+    uint8_t* xe;            // [T, d / 32] their E8M0 scales (MXFP4)
+    void* h;                // [T * k + T, inter_max] act dtype, or E4M3 codes (fp8 and MXFP4 weights)
     float* hs;              // [T * k + T, inter_max / 128] (fp8 weights only)
+    uint8_t* he;            // [T * k + T, inter_max / 32] E8M0 (MXFP4 weights only)
     void* y_rows;           // [T * k + T, d] act dtype: each row's expert output
     size_t total;
     int64_t max_tiles, nchunks, inter_max;
@@ -176,6 +178,10 @@ bool routing_is_fused(const moe_shape_t& s);
 hipError_t launch_routing_fused(const moe_shape_t& s, const float* logits, const uint8_t* allowed, int32_t* idx, float* w,
                                 int32_t* counts, int32_t* offsets, int32_t* sorted_slots, int32_t* pos,
                                 const Workspace& ws, int bm, TileRange tr, hipStream_t stream);
+// The permutation of a given routing: idx entries outside [0, E) are slots without an expert (pos -1), and slots
+// of one token that name the same expert share one row.  counts are rows per expert.
+hipError_t launch_permute_given(const moe_shape_t& s, const int32_t* idx, int32_t* counts, const Workspace& ws, int bm,
+                                TileRange tr, hipStream_t stream);
 hipError_t launch_permute(const moe_shape_t& s, const int32_t* idx, int32_t* counts, int32_t* offsets,
                           int32_t* sorted_slots, int32_t* pos, const Workspace& ws, int bm, TileRange tr,
                           hipStream_t stream);
@@ -188,6 +194,12 @@ hipError_t launch_up_gemm(const moe_shape_t& s, const void* x, const void* W1, c
                           const Workspace& ws, hipStream_t stream, int e_base, int n_shared);
 hipError_t launch_down_gemm(const moe_shape_t& s, const void* W2, const float* W2s, const void* S2, const float* S2s,
                             const Workspace& ws, hipStream_t stream, int e_base, int n_shared);
+// The same for MXFP4 weights (scale arguments: E8M0 bytes).
+hipError_t launch_up_gemm_mx(const moe_shape_t& s, const void* W1, const void* W3, const void* W1s, const void* W3s,
+                             const void* S1, const void* S3, const void* S1s, const void* S3s, const Workspace& ws,
+                             hipStream_t stream, int e_base, int n_shared);
+hipError_t launch_down_gemm_mx(const moe_shape_t& s, const void* W2, const void* W2s, const void* S2, const void* S2s,
+                               const Workspace& ws, hipStream_t stream, int e_base, int n_shared);
 hipError_t launch_combine_partial(const moe_shape_t& s, const int32_t* idx, const int32_t* pos, const float* w,
                                   const Workspace& ws, int e0, int e1, int with_shared, float* y_partial,
                                   hipStream_t stream);
@@ -200,5 +212,8 @@ hipError_t launch_dequantize_mx(int64_t n, bool fp4, bool bf16, const uint8_t* q
                                 hipStream_t stream);
 hipError_t launch_combine(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
                           hipStream_t stream);
+// pos entries of -1 are slots without an expert: they add nothing.
+hipError_t launch_combine_given(const moe_shape_t& s, const int32_t* pos, const float* w, const Workspace& ws, void* y,
+                                hipStream_t stream);
 
 }  // namespace moe

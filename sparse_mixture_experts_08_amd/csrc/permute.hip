@@ -54,8 +54,12 @@ __device__ void write_tiles(const int* cnt, const int* off, int E, int T, int k,
 // Fused path (T <= 256): one block of 1024 threads.
 // ---------------------------------------------------------------------------------------------------
 // SMALL_E: E <= 256 (16 lanes per token); otherwise a wavefront per token (E <= 1024).
-template <bool SMALL_E>
+// GIVEN: the routing is the caller's (given_idx; L, idx, w and sorted_slots unused).  A slot whose index lies
+// outside [0, E) gets pos -1 and no row; slots of a token that name the same expert set the same mask bit and
+// so share a row.
+template <bool SMALL_E, bool GIVEN>
 __global__ __launch_bounds__(1024) void route_fused_kernel(const float* __restrict__ L, const uint8_t* __restrict__ allowed,
+                                                           const int32_t* __restrict__ given_idx,
                                                            int T, int E, int k, int bm, TileRange tr,
                                                            int32_t* __restrict__ idx, float* __restrict__ w,
                                                            int32_t* __restrict__ counts, int32_t* __restrict__ offsets,
@@ -73,7 +77,16 @@ __global__ __launch_bounds__(1024) void route_fused_kernel(const float* __restri
     __syncthreads();
 
     // top-k: 16 lanes per token when E <= 256, else a whole wavefront per token
-    if constexpr (SMALL_E) {
+    if constexpr (GIVEN) {
+        for (int s = tid; s < T * k; s += 1024) {
+            const int e = given_idx[s], t = s / k, c = t >> 6, tl = t & 63;
+            const bool ok = e >= 0 && e < E;
+            idx_s[s] = ok ? e : -1;
+            if (!ok) continue;
+            if (tl < 32) atomicOr(&bits_lo[c][e], 1u << tl);
+            else atomicOr(&bits_hi[c][e], 1u << (tl - 32));
+        }
+    } else if constexpr (SMALL_E) {
         const int g = lane >> 4, sub = lane & 15;
         for (int t0 = wave * 4; t0 < T; t0 += 64) {
             const int t = t0 + g;
@@ -132,11 +145,15 @@ __global__ __launch_bounds__(1024) void route_fused_kernel(const float* __restri
     // scatter
     for (int s = tid; s < T * k; s += 1024) {
         const int t = s / k, e = idx_s[s], c = t >> 6, tl = t & 63;
+        if (GIVEN && e < 0) {
+            pos[s] = -1;
+            continue;
+        }
         const uint64_t mask = ((uint64_t)bits_hi[c][e] << 32) | bits_lo[c][e];
         const uint64_t below = tl ? (~0ull >> (64 - tl)) : 0ull;
         const int p = off[e] + cpre[c][e] + __popcll(mask & below);
         pos[s] = p;
-        sorted_slots[p] = s;
+        if constexpr (!GIVEN) sorted_slots[p] = s;
         row_token[p] = t;
     }
     for (int t = tid; t < T; t += 1024) row_token[T * k + t] = t;
@@ -169,7 +186,8 @@ __global__ __launch_bounds__(256) void chunk_scan_kernel(const int32_t* __restri
 // One thread per (token, slot) s: its sorted row is the expert's offset, plus the chunk prefix of earlier
 // chunks, plus the tokens of its own chunk below it in the expert's mask.  Every block first scans the E
 // counts into offsets in LDS (E <= 1024 values: cheaper than a grid-wide hand-off); block 0 also stores
-// the offsets and the tile list.  Threads s < T write the shared expert's row table.
+// the offsets and the tile list.  Threads s < T write the shared expert's row table.  GIVEN as above.
+template <bool GIVEN>
 __global__ __launch_bounds__(256) void scatter_kernel(const int32_t* __restrict__ idx, const uint64_t* __restrict__ chunk_bits,
                                                       const int32_t* __restrict__ chunk_prefix,
                                                       const int32_t* __restrict__ counts, int T, int E, int k, int bm,
@@ -205,12 +223,40 @@ __global__ __launch_bounds__(256) void scatter_kernel(const int32_t* __restrict_
     if (s >= T * k) return;
     const int t = s / k, c = t >> 6, tl = t & 63;
     const int e = idx[s];
+    if (GIVEN && (e < 0 || e >= E)) {
+        pos[s] = -1;
+        return;
+    }
     const size_t ce = (size_t)c * E + e;
     const uint64_t below = tl ? (~0ull >> (64 - tl)) : 0ull;
     const int p = off[e] + chunk_prefix[ce] + __popcll(chunk_bits[ce] & below);
     pos[s] = p;
-    sorted_slots[p] = s;
+    if constexpr (!GIVEN) sorted_slots[p] = s;
     row_token[p] = t;
+}
+
+// The masks of a given routing, one block per 64-token chunk (what the top-k kernel leaves for its own).
+__global__ __launch_bounds__(256) void given_bits_kernel(const int32_t* __restrict__ idx, int T, int E, int k,
+                                                         uint64_t* __restrict__ chunk_bits,
+                                                         int32_t* __restrict__ chunk_counts)
+{
+    __shared__ uint32_t bits_lo[1024], bits_hi[1024];
+    const int tid = threadIdx.x, c = blockIdx.x;
+    for (int e = tid; e < E; e += 256) bits_lo[e] = bits_hi[e] = 0;
+    __syncthreads();
+    const int n = min(64, T - c * 64) * k;
+    for (int i = tid; i < n; i += 256) {
+        const int e = idx[(size_t)c * 64 * k + i], tl = i / k;
+        if (e < 0 || e >= E) continue;
+        if (tl < 32) atomicOr(&bits_lo[e], 1u << tl);
+        else atomicOr(&bits_hi[e], 1u << (tl - 32));
+    }
+    __syncthreads();
+    for (int e = tid; e < E; e += 256) {
+        const uint64_t b = ((uint64_t)bits_hi[e] << 32) | bits_lo[e];
+        chunk_bits[(size_t)c * E + e] = b;
+        chunk_counts[(size_t)c * E + e] = __popcll(b);
+    }
 }
 
 bool routing_is_fused(const moe_shape_t& s) { return s.T <= kFusedMaxTokens; }
@@ -220,10 +266,10 @@ hipError_t launch_routing_fused(const moe_shape_t& s, const float* logits, const
                                 const Workspace& ws, int bm, TileRange tr, hipStream_t stream)
 {
     if (s.E <= 256)
-        route_fused_kernel<true><<<1, 1024, 0, stream>>>(logits, allowed, (int)s.T, (int)s.E, (int)s.k, bm, tr, idx, w, counts,
+        route_fused_kernel<true, false><<<1, 1024, 0, stream>>>(logits, allowed, nullptr, (int)s.T, (int)s.E, (int)s.k, bm, tr, idx, w, counts,
                                                          offsets, sorted_slots, pos, ws.row_token, ws.tiles, ws.sync);
     else
-        route_fused_kernel<false><<<1, 1024, 0, stream>>>(logits, allowed, (int)s.T, (int)s.E, (int)s.k, bm, tr, idx, w, counts,
+        route_fused_kernel<false, false><<<1, 1024, 0, stream>>>(logits, allowed, nullptr, (int)s.T, (int)s.E, (int)s.k, bm, tr, idx, w, counts,
                                                           offsets, sorted_slots, pos, ws.row_token, ws.tiles, ws.sync);
     return hipGetLastError();
 }
@@ -234,8 +280,25 @@ hipError_t launch_permute(const moe_shape_t& s, const int32_t* idx, int32_t* cou
 {
     const int T = (int)s.T, E = (int)s.E, k = (int)s.k, nch = (int)ws.nchunks;
     chunk_scan_kernel<<<E, 256, 0, stream>>>(ws.chunk_counts, nch, E, ws.chunk_prefix, counts);
-    scatter_kernel<<<(T * k + 255) / 256, 256, 0, stream>>>(idx, ws.chunk_bits, ws.chunk_prefix, counts, T, E, k, bm, tr,
+    scatter_kernel<false><<<(T * k + 255) / 256, 256, 0, stream>>>(idx, ws.chunk_bits, ws.chunk_prefix, counts, T, E, k, bm, tr,
                                                             offsets, sorted_slots, pos, ws.row_token, ws.tiles, ws.sync);
+    return hipGetLastError();
+}
+
+hipError_t launch_permute_given(const moe_shape_t& s, const int32_t* idx, int32_t* counts, const Workspace& ws, int bm,
+                                TileRange tr, hipStream_t stream)
+{
+    const int T = (int)s.T, E = (int)s.E, k = (int)s.k, nch = (int)ws.nchunks;
+    if (routing_is_fused(s)) {
+        route_fused_kernel<true, true><<<1, 1024, 0, stream>>>(nullptr, nullptr, idx, T, E, k, bm, tr, nullptr, nullptr, counts,
+                                                               ws.offsets, nullptr, ws.pos, ws.row_token, ws.tiles, ws.sync);
+        return hipGetLastError();
+    }
+    given_bits_kernel<<<nch, 256, 0, stream>>>(idx, T, E, k, ws.chunk_bits, ws.chunk_counts);
+    chunk_scan_kernel<<<E, 256, 0, stream>>>(ws.chunk_counts, nch, E, ws.chunk_prefix, counts);
+    scatter_kernel<true><<<(T * k + 255) / 256, 256, 0, stream>>>(idx, ws.chunk_bits, ws.chunk_prefix, counts, T, E, k, bm,
+                                                                  tr, ws.offsets, nullptr, ws.pos, ws.row_token, ws.tiles,
+                                                                  ws.sync);
     return hipGetLastError();
 }
 

@@ -11,6 +11,8 @@ Recipe (per tensor tag a torch.Generator seeded with seed * 1000 + tag id, on th
   bf16 tensors are the fp32 draws rounded to nearest-even by torch.
   fp8 tensors: per 128x128 block, s = U * amax / 448 with U ~ U[0.5, 2] (tag "U"), and the code is torch's
   float8_e4m3fn rounding of clamp(W / s, -448, 448).  (codes, scales) define the weight.
+  MXFP4 tensors: the fp32 draws in groups of 32 along the input features, each with the largest power of two not
+  above its amax, over 4, as its E8M0 scale, and the nearest E2M1 codes (ties to even, saturated), two to a byte.
   Skewed routing: bias[e] = -1.2 * ln(rank_e) over a seeded permutation pi (expert pi[r-1] has rank r),
   i.e. the logit bias log(p_e) + const for p_e proportional to rank_e^-1.2.
 Draws depend on the device (torch's CPU and GPU generators differ); every comparison draws once and
@@ -21,8 +23,8 @@ import math
 
 import torch
 
-F32, BF16, FP8_E4M3 = 0, 1, 2
-DTYPE_NAMES = {F32: "f32", BF16: "bf16", FP8_E4M3: "fp8_e4m3"}
+F32, BF16, FP8_E4M3, MXFP4 = 0, 1, 2, 3
+DTYPE_NAMES = {F32: "f32", BF16: "bf16", FP8_E4M3: "fp8_e4m3", MXFP4: "mxfp4"}
 
 _TAGS = {"x": 1, "Wg": 2, "W1": 3, "W3": 4, "W2": 5, "S1": 6, "S3": 7, "S2": 8, "perm": 9, "U": 10}
 
@@ -80,16 +82,32 @@ def _fp8_blocks(wf: torch.Tensor, u: torch.Tensor):
     return q.view(torch.uint8), s
 
 
+def _mx_groups(wf: torch.Tensor):
+    """fp32 [R, C] -> (E2M1 codes, two to a byte, uint8 [R, C/2]; E8M0 scales uint8 [R, C/32])."""
+    R, C = wf.shape
+    g = wf.view(R, C // 32, 32)
+    field = g.abs().amax(dim=-1).view(torch.int32) >> 23             # exponent field: floor(log2) + 127
+    code = (field - 2).clamp(min=0)
+    t = g * ((254 - code) << 23).view(torch.float32).unsqueeze(-1)   # / 2^(code - 127)
+    a = t.abs()
+    q = torch.where(a < 2, torch.round(2 * a), torch.where(a < 4, torch.round(a) + 2, torch.round(a / 2) + 4))
+    q = (q.clamp(max=7).to(torch.uint8) | (torch.signbit(t).to(torch.uint8) << 3)).view(R, C)
+    return q[:, 0::2] | (q[:, 1::2] << 4), code.to(torch.uint8)
+
+
 def _weight_stack(n, rows, cols, std, seed, tag, device, w_dtype, stack: bool):
     """n matrices [rows, cols] drawn one by one (bounded temporaries).  Returns (W, scales or None)."""
     g = _gen(seed, tag, device)
     gu = _gen(seed, "U", device) if w_dtype == FP8_E4M3 else None
     if gu is not None:  # separate U stream per tag: skip ahead by the tag id so tags differ
         gu.manual_seed(seed * 1000 + _TAGS["U"] * 100 + _TAGS[tag])
-    wdt = {F32: torch.float32, BF16: torch.bfloat16, FP8_E4M3: torch.uint8}[w_dtype]
-    shape = (n, rows, cols) if stack else (rows, cols)
+    wdt = {F32: torch.float32, BF16: torch.bfloat16, FP8_E4M3: torch.uint8, MXFP4: torch.uint8}[w_dtype]
+    stored = cols // 2 if w_dtype == MXFP4 else cols
+    shape = (n, rows, stored) if stack else (rows, stored)
     W = torch.empty(shape, dtype=wdt, device=device)
     S = None
+    if w_dtype == MXFP4:
+        S = torch.empty(((n,) if stack else ()) + (rows, cols // 32), dtype=torch.uint8, device=device)
     if w_dtype == FP8_E4M3:
         S = torch.empty(((n,) if stack else ()) + (rows // 128, cols // 128), dtype=torch.float32, device=device)
     for e in range(n if stack else 1):
@@ -98,6 +116,10 @@ def _weight_stack(n, rows, cols, std, seed, tag, device, w_dtype, stack: bool):
         if w_dtype == FP8_E4M3:
             u = torch.rand((rows // 128, cols // 128), generator=gu, device=device) * 1.5 + 0.5
             q, s = _fp8_blocks(wf, u)
+            dst.copy_(q)
+            (S[e] if stack else S).copy_(s)
+        elif w_dtype == MXFP4:
+            q, s = _mx_groups(wf)
             dst.copy_(q)
             (S[e] if stack else S).copy_(s)
         else:
@@ -118,7 +140,8 @@ def generate(wl: Workload, seed: int = 0, device="cpu", weights=True) -> dict:
 
     Keys: x [T,d]; Wg [E,d] fp32 (the gate's nn.Linear weight); bias [E] fp32 or None; W1, W3 [E,inter,d]; W2 [E,d,inter];
     S1, S3 [inter_s,d]; S2 [d,inter_s]; fp8 only: W1s, W3s [E,inter/128,d/128], W2s [E,d/128,inter/128],
-    S1s, S3s [inter_s/128,d/128], S2s [d/128,inter_s/128].
+    S1s, S3s [inter_s/128,d/128], S2s [d/128,inter_s/128].  MXFP4: weights [.., out, in/2] bytes, scales
+    [.., out, in/32] bytes.
     """
     act = torch.float32 if wl.act_dtype == F32 else torch.bfloat16
     out = {}

@@ -50,3 +50,57 @@ def pack(q):
 
 def unpack(b):
     return np.stack([b & 15, b >> 4], axis=-1).reshape(*b.shape[:-1], -1)
+
+
+def round_bf16(v):
+    """float64 -> nearest bf16 (ties to even), as float64.  The values met here are far inside bf16's range."""
+    m, e = np.frexp(v)
+    return np.ldexp(np.round(np.ldexp(m, 8)), e - 8)
+
+
+def entering(v, wtype):
+    """Activations v [rows, n] as a linear with weights of this type ("f32", "bf16", "fp8", "mxfp4") takes them."""
+    if wtype == "mxfp4":
+        return dequantize_mx(*quantize_mx(v, False), False)
+    if wtype == "fp8":
+        g = v.reshape(v.shape[0], -1, 128)
+        s = np.abs(g).max(axis=-1, keepdims=True).astype(np.float32) / np.float32(448)
+        s = np.where(s == 0, np.float32(1), s)
+        t = g.astype(np.float32) / s                      # the rule's fp32 division
+        q = E4M3[nearest_code(np.minimum(np.abs(t), 448).astype(np.float64), E4M3)] * np.sign(t)
+        return (q * s.astype(np.float64)).reshape(v.shape)
+    return v
+
+
+def weight(m, s, wtype):
+    """float64 values of one stored matrix (numpy: fp32, bf16 bits, or bytes) and its scales."""
+    if wtype == "mxfp4":
+        return dequantize_mx(unpack(m), s, True)
+    if wtype == "fp8":
+        v = np.where(m & 128, -np.append(E4M3, np.nan)[m & 127], np.append(E4M3, np.nan)[m & 127])
+        return v * np.repeat(np.repeat(s.astype(np.float64), 128, 0), 128, 1)
+    if wtype == "bf16":
+        return (m.astype(np.uint32) << 16).view(np.float32).astype(np.float64)
+    return m.astype(np.float64)
+
+
+def expert(xq, m1, m3, m2, wtype):
+    """A SwiGLU expert on rows xq (already as the first linears take them)."""
+    act = (lambda v: v) if wtype == "f32" else round_bf16
+    g, u = act(xq @ m1.T), act(xq @ m3.T)
+    h = act(g / (1 + np.exp(-g)) * u)
+    return act(entering(h, wtype) @ m2.T)
+
+
+def layer(h, x, idx, w, wtype):
+    """The layer for a given routing: h holds the stored weights by name (numpy), x [T, d] float64; y float64,
+    not rounded at the end.  Slots outside [0, E) add nothing."""
+    E = h["W1"].shape[0]
+    one = lambda n, e: weight(h[n][e], None if h.get(n + "s") is None else h[n + "s"][e], wtype)   # noqa: E731
+    xq = entering(x, wtype)
+    y = expert(xq, *(weight(h[n], h.get(n + "s"), wtype) for n in ("S1", "S3", "S2")), wtype)
+    for e in range(E):
+        t, j = np.nonzero(idx == e)
+        if len(t):
+            np.add.at(y, t, expert(xq[t], one("W1", e), one("W3", e), one("W2", e), wtype) * w[t, j][:, None].astype(np.float64))
+    return y
