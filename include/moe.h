@@ -199,6 +199,28 @@ moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const i
                                 hipStream_t stream);
 
 /*
+ * The whole layer for a few tokens (a decode step of one or a few sequences), T <= MOE_FEW_MAX_T, in two launches:
+ * moe_forward's arguments, types, routing rule, roundings and outputs, made for latency.
+ *  - Logits: the products are summed in fp64 with the bias, and the sum is rounded once to fp32.  moe_forward's
+ *    are an fp32 chain: where two logits lie within its error (some 1e-6) of each other the two may select
+ *    different experts.  Selection, ties (lower expert index) and softmax as moe_route.
+ *  - y differs from moe_forward's (for the same routing) by the order of the fp32 sums only, and is bitwise the
+ *    same from call to call.
+ *  - The workspace is the call's own: moe_few_workspace_size(shape) bytes (0 on a shape that moe_forward_few
+ *    does not take), 256-byte aligned, any contents.
+ * A larger T returns MOE_ERR_UNSUPPORTED; other errors as moe_forward.
+ */
+#define MOE_FEW_MAX_T 16
+size_t moe_few_workspace_size(const moe_shape_t* shape);
+moe_status_t moe_forward_few(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
+                             const void* W1, const void* W3, const void* W2,
+                             const void* W1s, const void* W3s, const void* W2s,
+                             const void* S1, const void* S3, const void* S2,
+                             const void* S1s, const void* S3s, const void* S2s,
+                             void* y, int32_t* idx_out, float* w_out, int32_t* counts_out,
+                             void* workspace, size_t workspace_bytes, hipStream_t stream);
+
+/*
  * fp8 activation quantisation, the layer's step for activations entering an fp8 linear (the fp8
  * configuration's 1 x 128 activation groups; "DeepSeek-V3.2-Exp / Mixture of experts / Shared expert",
  * the FP8 block-scale note under the parameter table: the checkpoint's weights carry block scales), on its

@@ -16,8 +16,10 @@ STATUS = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED", 3: "M
           5: "MOE_ERR_SCRATCH"}
 EXPORTS = ("moe_workspace_size", "moe_route", "moe_forward", "moe_forward_staged", "moe_route_limited",
            "moe_route_grouped", "moe_forward_shard", "moe_expert_utilization", "moe_forward_noalloc",
-           "moe_quantize_e4m3", "moe_quantize_mx", "moe_dequantize_mx", "moe_forward_routed", "moe_status_string")
+           "moe_quantize_e4m3", "moe_quantize_mx", "moe_dequantize_mx", "moe_forward_routed", "moe_few_workspace_size", "moe_forward_few",
+           "moe_status_string")
 NOALLOC_SCRATCH_BYTES = 64 << 20
+FEW_MAX_T = 16
 NUM_STAGES = 7
 STAGE_NAMES = ("router_logits", "topk_softmax", "permute", "x_quant", "up_gemm", "down_gemm", "combine")
 
@@ -67,6 +69,10 @@ def lib() -> ctypes.CDLL:
         L.moe_dequantize_mx.argtypes = [i64, i64, vp, vp, i32, i32, vp, vp]
         L.moe_forward_shard.restype = ctypes.c_int
         L.moe_forward_shard.argtypes = [sp] + [vp] * 4 + [i64] * 3 + [vp] * 17 + [ctypes.c_size_t, vp, vp]
+        L.moe_few_workspace_size.restype = ctypes.c_size_t
+        L.moe_few_workspace_size.argtypes = [sp]
+        L.moe_forward_few.restype = ctypes.c_int
+        L.moe_forward_few.argtypes = [sp] + [vp] * 20 + [ctypes.c_size_t, vp]
         L.moe_forward_routed.restype = ctypes.c_int
         L.moe_forward_routed.argtypes = [sp] + [vp] * 18 + [ctypes.c_size_t, vp]
         L.moe_expert_utilization.restype = ctypes.c_int
@@ -316,6 +322,41 @@ def moe_forward_routed(x, idx, w, W1, W3, W2, S1, S3, S2, scales=None, y=None, w
     if st:
         raise MoeError(st, "moe_forward_routed")
     return (y, c) if counts else y
+
+
+def moe_few_workspace_size(shape: moe_shape_t) -> int:
+    return int(lib().moe_few_workspace_size(ctypes.byref(shape)))
+
+
+def moe_forward_few(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, workspace=None, routing=False):
+    """moe_forward for at most FEW_MAX_T tokens, in two launches made for latency.  Arguments and results as
+    moe_forward; the workspace holds moe_few_workspace_size bytes."""
+    T, d = x.shape
+    E = W1.shape[0]
+    shape, sc, y = _layer(x, k, E, W1, W3, W2, S1, S3, S2, scales, y,
+                          [("Wg", Wg, torch.float32, (E, d)), ("bias", bias, torch.float32, (E,))])
+    dev = x.device
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = moe_few_workspace_size(shape)
+            if need == 0:
+                raise MoeError(2, "moe_few_workspace_size")
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        r = None
+        if routing:
+            r = dict(idx=torch.empty((T, k), dtype=torch.int32, device=dev),
+                     w=torch.empty((T, k), dtype=torch.float32, device=dev),
+                     counts=torch.empty(E, dtype=torch.int32, device=dev))
+            if T == 0:
+                r["counts"].zero_()                    # no tokens: the library writes nothing
+        st = lib().moe_forward_few(ctypes.byref(shape), _ptr(x), _ptr(Wg), _ptr(bias), _ptr(W1), _ptr(W3), _ptr(W2),
+                                   *[_ptr(sc.get(n)) for n in _SCALES[:3]], _ptr(S1), _ptr(S3), _ptr(S2),
+                                   *[_ptr(sc.get(n)) for n in _SCALES[3:]], _ptr(y), _ptr(r and r["idx"]),
+                                   _ptr(r and r["w"]), _ptr(r and r["counts"]), _ptr(workspace), workspace.numel(),
+                                   _stream(dev))
+    if st:
+        raise MoeError(st, "moe_forward_few")
+    return (y, r) if routing else y
 
 
 def moe_forward_noalloc(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None, routing=False):

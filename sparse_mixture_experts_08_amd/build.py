@@ -12,7 +12,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
-SOURCES = ["moe_abi.hip", "router.hip", "permute.hip", "gemm.hip", "combine.hip", "mx.hip", "mx_gemm.hip"]
+SOURCES = ["moe_abi.hip", "router.hip", "permute.hip", "gemm.hip", "combine.hip", "mx.hip", "mx_gemm.hip", "few.hip"]
 PROBE_LIB = os.path.join(HERE, "libmoe_probe.so")
 PROBE_SOURCES = ["peak_probe.hip"]
 

@@ -348,6 +348,38 @@ extern "C" moe_status_t moe_forward_routed(const moe_shape_t* shape, const void*
                       stream, nullptr, &given);
 }
 
+// What moe_forward_few takes besides check_shape: few tokens, and K units of 128 in its 32-bit row arithmetic.
+static moe_status_t check_few(const moe_shape_t* s)
+{
+    const moe_status_t st = check_shape(s);
+    if (st != MOE_OK) return st;
+    return s->T > MOE_FEW_MAX_T ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+extern "C" size_t moe_few_workspace_size(const moe_shape_t* shape)
+{
+    return check_few(shape) == MOE_OK ? few_workspace_bytes(*shape) : 0;
+}
+
+extern "C" moe_status_t moe_forward_few(const moe_shape_t* shape, const void* x, const float* Wg, const float* bias,
+                                        const void* W1, const void* W3, const void* W2, const void* W1s,
+                                        const void* W3s, const void* W2s, const void* S1, const void* S3,
+                                        const void* S2, const void* S1s, const void* S3s, const void* S2s, void* y,
+                                        int32_t* idx_out, float* w_out, int32_t* counts_out, void* workspace,
+                                        size_t workspace_bytes, hipStream_t stream)
+{
+    moe_status_t st = check_few(shape);
+    if (st != MOE_OK) return st;
+    st = check_layer_args(shape, x, Wg, 0, shape->E, shape->inter_shared, W1, W3, W2, W1s, W3s, W2s, S1, S3, S2, S1s,
+                          S3s, S2s, y);
+    if (st != MOE_OK || shape->T == 0) return st;
+    if (!workspace) return MOE_ERR_INVALID_ARG;
+    if (workspace_bytes < few_workspace_bytes(*shape) || ((uintptr_t)workspace & 255)) return MOE_ERR_WORKSPACE;
+    const FewWeights m = {W1, W3, W2, W1s, W3s, W2s, S1, S3, S2, S1s, S3s, S2s};
+    MOE_TRY(launch_few(*shape, x, Wg, bias, m, y, idx_out, w_out, counts_out, workspace, stream));
+    return MOE_OK;
+}
+
 extern "C" moe_status_t moe_quantize_e4m3(int64_t rows, int64_t cols, const void* x, uint8_t* q, float* scales,
                                           hipStream_t stream)
 {

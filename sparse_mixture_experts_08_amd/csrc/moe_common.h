@@ -205,6 +205,13 @@ hipError_t launch_combine_partial(const moe_shape_t& s, const int32_t* idx, cons
                                   hipStream_t stream);
 hipError_t launch_expert_utilization(int E, const int32_t* counts, float* util, int32_t* flags, int32_t* summary,
                                      hipStream_t stream);
+// The few-token layer (T <= MOE_FEW_MAX_T): its own workspace and both of its launches.
+struct FewWeights {
+    const void *W1, *W3, *W2, *W1s, *W3s, *W2s, *S1, *S3, *S2, *S1s, *S3s, *S2s;
+};
+size_t few_workspace_bytes(const moe_shape_t& s);
+hipError_t launch_few(const moe_shape_t& s, const void* x, const float* Wg, const float* bias, const FewWeights& m, void* y,
+                      int32_t* idx_out, float* w_out, int32_t* counts_out, void* workspace, hipStream_t stream);
 // n elements (a multiple of 32) to or from a microscaled format; bf16: the other side is bf16, else fp32.
 hipError_t launch_quantize_mx(int64_t n, bool fp4, bool bf16, const void* x, uint8_t* q, uint8_t* scales,
                               hipStream_t stream);

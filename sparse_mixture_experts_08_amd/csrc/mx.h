@@ -61,6 +61,28 @@ __device__ __forceinline__ uint2 mx_pack_fp8(const float (&v)[8], uint32_t c)
                       f32x2_to_e4m3(t[4], t[5]) | (f32x2_to_e4m3(t[6], t[7]) << 16));
 }
 
+// Eight of a 128-element group's values (16 lanes hold the group) as E4M3 codes by the fp8 layer's rule, s = amax /
+// 448 in fp32 (1 for a group of zeros), codes of v / s; s to every lane.
+__device__ __forceinline__ uint2 quant8_e4m3(const float (&v)[8], float& s)
+{
+    float amax = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(v[e]));
+    amax = row16_max(amax);
+    s = amax > 0.f ? amax / 448.0f : 1.0f;
+    float t[8];
+    if (quant_div_fast(s)) {
+        const float r = recip_rn(s);
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = quant_div(v[e], s, r);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; e++) t[e] = v[e] / s;
+    }
+    return make_uint2(f32x2_to_e4m3(t[0], t[1]) | (f32x2_to_e4m3(t[2], t[3]) << 16),
+                      f32x2_to_e4m3(t[4], t[5]) | (f32x2_to_e4m3(t[6], t[7]) << 16));
+}
+
 // Bit pattern maximum of the magnitudes of eight values.
 __device__ __forceinline__ uint32_t mx_amax8(const float (&v)[8])
 {
