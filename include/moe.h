@@ -188,7 +188,9 @@ moe_status_t moe_route_limited(const moe_shape_t* shape, const void* x, const fl
  *   counts_out [E] int32 rows per expert (a token that names an expert twice is one row), or NULL
  * y[t] = sum_j w[t][j] * SwiGLU_{idx[t][j]}(x[t]) + SwiGLU_shared(x[t]), the sum over j by ascending expert.
  * All other arguments, roundings, guarantees and errors as moe_forward; moe_workspace_size applies.  With the idx
- * and w that moe_forward reports, y is moe_forward's bit for bit.
+ * and w that moe_forward reports, y is moe_forward's bit for bit, but for fp8 weights: the activation scales are
+ * s = amax * (1/448) in fp32 here, what a torch program on the GPU gets for amax / 448.0, so that the codes agree
+ * with such a program's.  s is within an ulp of moe_forward's; values between two codes may go the other way.
  */
 moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const int32_t* idx, const float* w,
                                 const void* W1, const void* W3, const void* W2,
@@ -204,8 +206,8 @@ moe_status_t moe_forward_routed(const moe_shape_t* shape, const void* x, const i
  *  - Logits: the products are summed in fp64 with the bias, and the sum is rounded once to fp32.  moe_forward's
  *    are an fp32 chain: where two logits lie within its error (some 1e-6) of each other the two may select
  *    different experts.  Selection, ties (lower expert index) and softmax as moe_route.
- *  - y differs from moe_forward's (for the same routing) by the order of the fp32 sums only, and is bitwise the
- *    same from call to call.
+ *  - y differs from moe_forward's (for the same routing) by the order of the fp32 sums, and with fp8 weights by
+ *    the activation scales' rule, which is moe_forward_routed's; it is bitwise the same from call to call.
  *  - The workspace is the call's own: moe_few_workspace_size(shape) bytes (0 on a shape that moe_forward_few
  *    does not take), 256-byte aligned, any contents.
  * A larger T returns MOE_ERR_UNSUPPORTED; other errors as moe_forward.

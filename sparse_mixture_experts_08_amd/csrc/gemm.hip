@@ -131,7 +131,7 @@ __device__ __forceinline__ void mma_stage(const uint8_t* As_lds, const uint8_t* 
 // Epilogue of the 16x16-MFMA kernels.  Accumulator layout: lane holds rows 4*(lane/16) + r, column
 // lane % 16.  UP: h = round(silu(round g) * round u), with fp8 weights quantised per 1x128 group through
 // `smem` (BM x BN floats; the caller has finished with the staging buffers); down: y rows = round(acc).
-template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WM, int WN, int NT>
+template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WM, int WN, int NT, bool RECIP>
 __device__ __forceinline__ void gemm_epilogue(const GemmArgs& g, uint8_t* smem, const f32x4 (&acc1)[WM][WN],
                                               const f32x4 (&acc3)[WM][WN], int rows, int row0, int n0, int wm0,
                                               int wn0, int tid)
@@ -162,7 +162,7 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs& g, uint8_t* smem, 
 #pragma unroll
             for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(v[e]));
             amax = row16_max(amax);
-            const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+            const float sc = f8_act_scale<RECIP>(amax);
             if (row < rows) {
                 float q[8];
                 if (quant_div_fast(sc)) {
@@ -207,8 +207,8 @@ __device__ __forceinline__ void gemm_epilogue(const GemmArgs& g, uint8_t* smem, 
 
 // NBUF: LDS stages (2 = double buffered, one barrier per K stage; 1 = single buffer, two barriers per
 // stage but half the LDS, so two blocks share a CU and cover each other's barriers).  MINW: minimum
-// wavefronts per SIMD the register allocation must allow.
-template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, int MINW>
+// wavefronts per SIMD the register allocation must allow.  RECIP: the rule of h's fp8 scales (f8_act_scale).
+template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF, int MINW, bool RECIP>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, MINW) void grouped_gemm_kernel(GemmArgs g)
 {
     constexpr int NB = UP ? 2 * BN : BN;               // B rows per stage
@@ -405,7 +405,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N, MINW) void grouped_gemm_ker
         __syncthreads();
     }
 
-    gemm_epilogue<ET, UP, ACT_BF16, BM, BN, WM, WN, NT>(g, smem, acc1, acc3, rows, row0, n0, wm0, wn0, tid);
+    gemm_epilogue<ET, UP, ACT_BF16, BM, BN, WM, WN, NT, RECIP>(g, smem, acc1, acc3, rows, row0, n0, wm0, wn0, tid);
 }
 
 // ---------------------------------------------------------------------------------------------------
@@ -832,7 +832,7 @@ __device__ __forceinline__ void mma_f8(const uint8_t* As_lds, const uint8_t* Bs_
 // (BM x BN floats, each row's 16-byte chunks XOR-swizzled by token so a wavefront's 16 tokens write
 // distinct banks), then quantised per 1 x 128 group to E4M3 codes plus one scale per group.  Down: the
 // bf16 output tile through LDS (padded rows), then whole-line copies to the output rows.
-template <bool UP, int BM, int BN, int WM, int WN, int NT>
+template <bool UP, int BM, int BN, int WM, int WN, int NT, bool RECIP>
 __device__ __forceinline__ void f8_epilogue(const GemmArgs& g, uint8_t* smem, const f32x4 (&acc1)[WM][WN],
                                             const f32x4 (&acc3)[WM][WN], int rows, int row0, int n0, int wm0,
                                             int wn0, int tid)
@@ -876,7 +876,7 @@ __device__ __forceinline__ void f8_epilogue(const GemmArgs& g, uint8_t* smem, co
 #pragma unroll
             for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(v[e]));
             amax = row16_max(amax);
-            const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+            const float sc = f8_act_scale<RECIP>(amax);
             if (row < rows) {
                 float q[8];
                 if (quant_div_fast(sc)) {
@@ -919,7 +919,7 @@ __device__ __forceinline__ void f8_epilogue(const GemmArgs& g, uint8_t* smem, co
 // row), wavefront 2 the W1 block scales, wavefront 3 the W3 block scales, the others a dummy copy, so
 // every wavefront issues the same number of loads per stage and one vmcnt value waits for a stage.
 // ---------------------------------------------------------------------------------------------------
-template <bool UP, int BM, int BN, int NSTG>
+template <bool UP, int BM, int BN, int NSTG, bool RECIP>
 __global__ __launch_bounds__(512, 2) void grouped_gemm_f8_kernel(GemmArgs g)
 {
     constexpr int WAVES_M = 2, WAVES_N = 4, NW = 8, NT = 512;
@@ -1054,11 +1054,12 @@ __global__ __launch_bounds__(512, 2) void grouped_gemm_f8_kernel(GemmArgs g)
     with_count<WM>(nrb, k_walk);
     wait_vmcnt<0>();                                   // no load may still target this block's LDS
     lds_barrier();
-    f8_epilogue<UP, BM, BN, WM, WN, NT>(g, ring, acc1, acc3, rows, row0, n0, wm0, wn0, tid);
+    f8_epilogue<UP, BM, BN, WM, WN, NT, RECIP>(g, ring, acc1, acc3, rows, row0, n0, wm0, wn0, tid);
 }
 
 // fp8 activation quantisation of x: per row, per 128-column group, s = amax / 448 (1 if amax = 0),
 // codes = E4M3(round to nearest even)(x / s).  16 threads per group, 8 elements each.
+template <bool RECIP>
 __global__ __launch_bounds__(256) void act_quant_kernel(const uint16_t* __restrict__ x, int64_t ngroups, int d,
                                                         uint8_t* __restrict__ xq, float* __restrict__ xs)
 {
@@ -1078,7 +1079,7 @@ __global__ __launch_bounds__(256) void act_quant_kernel(const uint16_t* __restri
 #pragma unroll
     for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(v[e]));
     amax = row16_max(amax);
-    const float sc = amax > 0.f ? amax / 448.0f : 1.0f;
+    const float sc = f8_act_scale<RECIP>(amax);
     float q[8];
     if (quant_div_fast(sc)) {
         const float r = recip_rn(sc);
@@ -1094,23 +1095,27 @@ __global__ __launch_bounds__(256) void act_quant_kernel(const uint16_t* __restri
     if (sub == 0) xs[gi] = sc;
 }
 
-hipError_t launch_quantize_e4m3(int64_t rows, int cols, const void* x, uint8_t* q, float* scales, hipStream_t stream)
+hipError_t launch_quantize_e4m3(int64_t rows, int cols, const void* x, uint8_t* q, float* scales, hipStream_t stream,
+                                bool recip)
 {
     const int64_t ngroups = rows * (cols / 128);
-    act_quant_kernel<<<(unsigned)((ngroups + 15) / 16), 256, 0, stream>>>((const uint16_t*)x, ngroups, cols, q, scales);
+    const unsigned grid = (unsigned)((ngroups + 15) / 16);
+    if (recip) act_quant_kernel<true><<<grid, 256, 0, stream>>>((const uint16_t*)x, ngroups, cols, q, scales);
+    else act_quant_kernel<false><<<grid, 256, 0, stream>>>((const uint16_t*)x, ngroups, cols, q, scales);
     return hipGetLastError();
 }
 
-hipError_t launch_act_quant(const moe_shape_t& s, const void* x, const Workspace& ws, hipStream_t stream)
+hipError_t launch_act_quant(const moe_shape_t& s, const void* x, const Workspace& ws, hipStream_t stream, bool recip)
 {
-    return launch_quantize_e4m3(s.T, (int)s.d, x, ws.xq, ws.xs, stream);
+    return launch_quantize_e4m3(s.T, (int)s.d, x, ws.xq, ws.xs, stream, recip);
 }
 
-template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF = 2, int MINW = 1>
+template <int ET, bool UP, bool ACT_BF16, int BM, int BN, int WAVES_M, int WAVES_N, int NBUF = 2, int MINW = 1,
+          bool RECIP = false>
 static void launch_one(GemmArgs a, hipStream_t stream)
 {
     const int64_t nblk = launch_blocks(a);
-    grouped_gemm_kernel<ET, UP, ACT_BF16, BM, BN, WAVES_M, WAVES_N, NBUF, MINW>
+    grouped_gemm_kernel<ET, UP, ACT_BF16, BM, BN, WAVES_M, WAVES_N, NBUF, MINW, RECIP>
         <<<(unsigned)nblk, 64 * WAVES_M * WAVES_N, 0, stream>>>(a);
 }
 
@@ -1140,11 +1145,11 @@ static void launch_w(GemmArgs a, hipStream_t stream)
 }
 
 // fp8 tiles of 128 or 256 rows: a ring of three stages for 128-row tiles, two for 256 (LDS).
-template <bool UP, int BM, int BN>
+template <bool UP, int BM, int BN, bool RECIP = false>
 static void launch_f8(GemmArgs a, hipStream_t stream)
 {
     const int64_t nblk = launch_blocks(a);
-    grouped_gemm_f8_kernel<UP, BM, BN, BM == 128 ? 3 : 2><<<(unsigned)nblk, 512, 0, stream>>>(a);
+    grouped_gemm_f8_kernel<UP, BM, BN, BM == 128 ? 3 : 2, RECIP><<<(unsigned)nblk, 512, 0, stream>>>(a);
 }
 
 // 16-row tiles (bf16): output features per block, wavefronts, minimum wavefronts per SIMD.  inter and
@@ -1176,7 +1181,7 @@ static GemmArgs base_args(const moe_shape_t& s, const Workspace& ws, int e_base)
 //   fp8, 128/256-row      grouped_gemm_f8_kernel
 hipError_t launch_up_gemm(const moe_shape_t& s, const void* x, const void* W1, const void* W3, const float* W1s,
                           const float* W3s, const void* S1, const void* S3, const float* S1s, const float* S3s,
-                          const Workspace& ws, hipStream_t stream, int e_base, int n_shared)
+                          const Workspace& ws, hipStream_t stream, int e_base, int n_shared, bool recip)
 {
     const bool fp8 = s.w_dtype == MOE_FP8_E4M3, f32 = s.act_dtype == MOE_F32;
     const int64_t act = f32 ? 4 : 2;
@@ -1216,7 +1221,11 @@ hipError_t launch_up_gemm(const moe_shape_t& s, const void* x, const void* W1, c
     }
     if (fp8) {
         up.n_blocks = (int)(ws.inter_max / 128);
-        if (bm == 16) launch_one<ET_FP8, true, true, 16, 128, 1, 4>(up, stream);
+        if (recip) {
+            if (bm == 16) launch_one<ET_FP8, true, true, 16, 128, 1, 4, 2, 1, true>(up, stream);
+            else if (bm == 128) launch_f8<true, 128, 128, true>(up, stream);
+            else launch_f8<true, 256, 128, true>(up, stream);
+        } else if (bm == 16) launch_one<ET_FP8, true, true, 16, 128, 1, 4>(up, stream);
         else if (bm == 128) launch_f8<true, 128, 128>(up, stream);
         else launch_f8<true, 256, 128>(up, stream);
     } else if (f32) {

@@ -278,12 +278,12 @@ static moe_status_t layer_impl(const moe_shape_t* shape, const void* x, const fl
         }
     }
     MOE_TRY(mark(3));
-    if (fp8) MOE_TRY(launch_act_quant(s, x, ws, stream));
+    if (fp8) MOE_TRY(launch_act_quant(s, x, ws, stream, given != nullptr));
     if (mx) MOE_TRY(launch_quantize_mx(s.T * s.d, false, true, x, ws.xq, ws.xe, stream));
     MOE_TRY(mark(4));
     if (mx) MOE_TRY(launch_up_gemm_mx(s, W1, W3, W1s, W3s, S1, S3, S1s, S3s, ws, stream, (int)e0, (int)n_shared));
     else MOE_TRY(launch_up_gemm(s, x, W1, W3, (const float*)W1s, (const float*)W3s, S1, S3, (const float*)S1s,
-                                (const float*)S3s, ws, stream, (int)e0, (int)n_shared));
+                                (const float*)S3s, ws, stream, (int)e0, (int)n_shared, given != nullptr));
     MOE_TRY(mark(5));
     if (mx) MOE_TRY(launch_down_gemm_mx(s, W2, W2s, S2, S2s, ws, stream, (int)e0, (int)n_shared));
     else MOE_TRY(launch_down_gemm(s, W2, (const float*)W2s, S2, (const float*)S2s, ws, stream, (int)e0, (int)n_shared));

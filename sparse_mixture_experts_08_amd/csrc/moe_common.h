@@ -65,6 +65,16 @@ __device__ __forceinline__ float quant_div(float v, float s, float r)
     return __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-s, q0, v), r, q0), v);
 }
 
+// Scale of an fp8 activation group with maximum amax: amax / 448 (1 for a group of zeros).  RECIP: amax * (1 / 448) in
+// fp32, which is what a torch program on the GPU gets for `amax / 448.0` (it divides by a number through its
+// reciprocal) and within an ulp of the quotient.  An ulp matters here: bf16 values often lie exactly between two
+// codes, and those go the other way (0.1 % of the codes of normally distributed rows), which the second
+// quantisation of the layer amplifies to 1 to 2 % of y.
+template <bool RECIP> __device__ __forceinline__ float f8_act_scale(float amax)
+{
+    return amax > 0.f ? (RECIP ? amax * (1.0f / 448.0f) : amax / 448.0f) : 1.0f;
+}
+
 // Maximum of a non-negative, non-NaN x over each aligned group of 16 lanes (a DPP row), returned to every
 // lane of the group: four DPP moves (the neighbour in a pair, the other pair of a quad, the mirrored quad
 // of a half-row, the mirrored half-row) instead of four LDS permutes.  Such floats order as their bit
@@ -185,13 +195,15 @@ hipError_t launch_permute_given(const moe_shape_t& s, const int32_t* idx, int32_
 hipError_t launch_permute(const moe_shape_t& s, const int32_t* idx, int32_t* counts, int32_t* offsets,
                           int32_t* sorted_slots, int32_t* pos, const Workspace& ws, int bm, TileRange tr,
                           hipStream_t stream);
-hipError_t launch_act_quant(const moe_shape_t& s, const void* x, const Workspace& ws, hipStream_t stream);
-hipError_t launch_quantize_e4m3(int64_t rows, int cols, const void* x, uint8_t* q, float* scales, hipStream_t stream);
+// recip: the activation scales' rule (f8_act_scale).
+hipError_t launch_act_quant(const moe_shape_t& s, const void* x, const Workspace& ws, hipStream_t stream, bool recip);
+hipError_t launch_quantize_e4m3(int64_t rows, int cols, const void* x, uint8_t* q, float* scales, hipStream_t stream,
+                                bool recip = false);
 // e_base: the expert stored first in W1/W3/W2 (0 for the whole layer); n_shared: the shared hidden
 // features held in S1/S3 ([n_shared, d]) and S2 ([d, n_shared]).
 hipError_t launch_up_gemm(const moe_shape_t& s, const void* x, const void* W1, const void* W3, const float* W1s,
                           const float* W3s, const void* S1, const void* S3, const float* S1s, const float* S3s,
-                          const Workspace& ws, hipStream_t stream, int e_base, int n_shared);
+                          const Workspace& ws, hipStream_t stream, int e_base, int n_shared, bool recip = false);
 hipError_t launch_down_gemm(const moe_shape_t& s, const void* W2, const float* W2s, const void* S2, const float* S2s,
                             const Workspace& ws, hipStream_t stream, int e_base, int n_shared);
 // The same for MXFP4 weights (scale arguments: E8M0 bytes).

@@ -61,15 +61,15 @@ __device__ __forceinline__ uint2 mx_pack_fp8(const float (&v)[8], uint32_t c)
                       f32x2_to_e4m3(t[4], t[5]) | (f32x2_to_e4m3(t[6], t[7]) << 16));
 }
 
-// Eight of a 128-element group's values (16 lanes hold the group) as E4M3 codes by the fp8 layer's rule, s = amax /
-// 448 in fp32 (1 for a group of zeros), codes of v / s; s to every lane.
+// Eight of a 128-element group's values (16 lanes hold the group) as E4M3 codes of v / s, s = f8_act_scale<true>;
+// s to every lane.
 __device__ __forceinline__ uint2 quant8_e4m3(const float (&v)[8], float& s)
 {
     float amax = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(v[e]));
     amax = row16_max(amax);
-    s = amax > 0.f ? amax / 448.0f : 1.0f;
+    s = f8_act_scale<true>(amax);
     float t[8];
     if (quant_div_fast(s)) {
         const float r = recip_rn(s);

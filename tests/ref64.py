@@ -64,9 +64,9 @@ def entering(v, wtype):
         return dequantize_mx(*quantize_mx(v, False), False)
     if wtype == "fp8":
         g = v.reshape(v.shape[0], -1, 128)
-        s = np.abs(g).max(axis=-1, keepdims=True).astype(np.float32) / np.float32(448)
+        s = np.abs(g).max(axis=-1, keepdims=True).astype(np.float32) * (np.float32(1) / np.float32(448))
         s = np.where(s == 0, np.float32(1), s)
-        t = g.astype(np.float32) / s                      # the rule's fp32 division
+        t = g.astype(np.float32) / s                      # the rule's fp32 quotient
         q = E4M3[nearest_code(np.minimum(np.abs(t), 448).astype(np.float64), E4M3)] * np.sign(t)
         return (q * s.astype(np.float64)).reshape(v.shape)
     return v
