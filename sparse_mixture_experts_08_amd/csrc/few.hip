@@ -35,8 +35,9 @@ constexpr int FEW_T = MOE_FEW_MAX_T;
 constexpr int FEW_SLOTS = FEW_T * 16;                  // (token, slot) pairs at most
 constexpr int FEW_GROUPS = FEW_SLOTS + 1;              // selected experts and the shared one, at most
 constexpr int FEW_NW = 8;                              // wavefronts per block of launch 2
-constexpr int FEW_UP = 16;                             // hidden features per up item
+constexpr int FEW_UP = 8;                              // hidden features a wavefront in an up item
 constexpr int FEW_DN = 16 * FEW_NW;                    // output features per down item
+constexpr int FEW_PAD = 16;                            // ints between counters: a 64-byte line each
 
 struct FewArgs {
     int T, d, E, k, inter, inter_s, inter_max;
@@ -49,13 +50,15 @@ struct FewArgs {
     uint8_t* y_rows;                                   // [T k + T, d] act dtype
     uint8_t* y;
     int32_t *idx_out, *w_out_bits, *counts_out;        // optional
-    int32_t *ticket, *up_done, *col_done;              // counters: [1], [FEW_GROUPS], [d / FEW_DN]
+    int32_t *ticket, *up_done, *col_done;              // counters: [1], [FEW_GROUPS], [d / FEW_DN], FEW_PAD apart
 };
 
 // ---------------------------------------------------------------------------------------------------
 // Launch 1.  Blocks [0, E): the logits of one expert for every token.  Blocks [E, E + nq): quantisation of x.
 // The last block clears the counters.
 // ---------------------------------------------------------------------------------------------------
+constexpr int FEW_NT1 = 512;                           // threads per block of launch 1
+
 template <typename XT> __device__ __forceinline__ void load4(const XT* p, double (&v)[4]);
 template <> __device__ __forceinline__ void load4<uint16_t>(const uint16_t* p, double (&v)[4])
 {
@@ -71,23 +74,43 @@ template <> __device__ __forceinline__ void load4<float>(const float* p, double 
     v[0] = (double)r.x; v[1] = (double)r.y; v[2] = (double)r.z; v[3] = (double)r.w;
 }
 
+// Sums of TM values over a wavefront, value t to the lanes whose top log2(TM) bits are t (bit 5 first): each step
+// halves the values that a lane keeps and adds the partner's, so TM values take TM - 1 exchanges and then one per
+// remaining bit, against 6 TM.
+template <int TM> __device__ __forceinline__ double wave_sums(double (&v)[TM], int lane)
+{
+    int off = 32;
+#pragma unroll
+    for (int n = TM / 2; n >= 1; n >>= 1, off >>= 1) {
+        const bool hi = lane & off;
+#pragma unroll
+        for (int i = 0; i < n; i++) {
+            const double other = __shfl_xor(hi ? v[i] : v[n + i], off, 64);
+            v[i] = (hi ? v[n + i] : v[i]) + other;
+        }
+    }
+#pragma unroll
+    for (int o = 32 / TM; o >= 1; o >>= 1) v[0] += __shfl_xor(v[0], o, 64);
+    return v[0];
+}
+
 template <int ST, int TM>
-__global__ __launch_bounds__(256) void few_prepare_kernel(const void* __restrict__ xv, const float* __restrict__ Wg,
-                                                          const float* __restrict__ bias, float* __restrict__ logits,
-                                                          int T, int d, int E, uint8_t* __restrict__ xq,
-                                                          uint8_t* __restrict__ xs, int32_t* __restrict__ counters,
-                                                          int n_counters)
+__global__ __launch_bounds__(FEW_NT1) void few_prepare_kernel(const void* __restrict__ xv, const float* __restrict__ Wg,
+                                                              const float* __restrict__ bias, float* __restrict__ logits,
+                                                              int T, int d, int E, uint8_t* __restrict__ xq,
+                                                              uint8_t* __restrict__ xs, int32_t* __restrict__ counters,
+                                                              int n_counters)
 {
     typedef typename std::conditional<ST == ST_F32, float, uint16_t>::type XT;
     const XT* x = (const XT*)xv;
     const int tid = threadIdx.x, b = blockIdx.x;
     if (b < E) {
-        __shared__ double part[4][TM];
+        __shared__ double part[FEW_NT1 / 64][TM];
         double acc[TM];
 #pragma unroll
         for (int t = 0; t < TM; t++) acc[t] = 0.0;
         const float* wrow = Wg + (size_t)b * d;
-        for (int i = tid * 4; i < d; i += 1024) {
+        for (int i = tid * 4; i < d; i += 4 * FEW_NT1) {
             double w[4];
             load4<float>(wrow + i, w);
 #pragma unroll
@@ -98,36 +121,32 @@ __global__ __launch_bounds__(256) void few_prepare_kernel(const void* __restrict
                 for (int e = 0; e < 4; e++) acc[t] = __builtin_fma(v[e], w[e], acc[t]);
             }
         }
-#pragma unroll
-        for (int t = 0; t < TM; t++) {
-#pragma unroll
-            for (int off = 32; off >= 1; off >>= 1) acc[t] += __shfl_xor(acc[t], off, 64);
-            if ((tid & 63) == 0) part[tid >> 6][t] = acc[t];
-        }
+        const int lane = tid & 63;
+        const double s = wave_sums<TM>(acc, lane);
+        if (lane % (64 / TM) == 0) part[tid >> 6][lane / (64 / TM)] = s;
         __syncthreads();
         if (tid < T) {
-            double s = ((part[0][tid] + part[1][tid]) + part[2][tid]) + part[3][tid];
+            double s = part[0][tid];
+#pragma unroll
+            for (int w = 1; w < FEW_NT1 / 64; w++) s += part[w][tid];
             if (bias) s += (double)bias[b];
             logits[(size_t)tid * E + b] = (float)s;
         }
         return;
     }
     if (b == (int)gridDim.x - 1) {
-        for (int i = tid; i < n_counters; i += 256) counters[i] = 0;
+        for (int i = tid; i < n_counters; i += FEW_NT1) counters[i] = 0;
         return;
     }
+    const int64_t i = (int64_t)(b - E) * FEW_NT1 + tid;                // eight elements each
+    if (i >= (int64_t)T * d / 8) return;                               // whole groups of 16 lanes leave together
+    float v[8];
     if constexpr (ST == ST_MX4) {
-        const int64_t i = (int64_t)(b - E) * 256 + tid;               // eight elements each
-        if (i >= (int64_t)T * d / 8) return;                           // whole groups of 16 lanes leave together
-        float v[8];
         bf16x8_to_f32(((const uint4*)x)[i], v);
         const uint32_t c = mx_scale_code<false>(quad_max(mx_amax8(v)));
         ((uint2*)xq)[i] = c == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(v, c);
         if ((i & 3) == 0) xs[i >> 2] = (uint8_t)c;
     } else if constexpr (ST == ST_FP8) {
-        const int64_t i = (int64_t)(b - E) * 256 + tid;
-        if (i >= (int64_t)T * d / 8) return;
-        float v[8];
         bf16x8_to_f32(((const uint4*)x)[i], v);
         float sc;
         ((uint2*)xq)[i] = quant8_e4m3(v, sc);
@@ -138,43 +157,78 @@ __global__ __launch_bounds__(256) void few_prepare_kernel(const void* __restrict
 // ---------------------------------------------------------------------------------------------------
 // Launch 2.
 // ---------------------------------------------------------------------------------------------------
-template <int ST> struct FewH;                         // the chunk of h that a down item keeps in LDS
-template <> struct FewH<ST_F32> { static constexpr int KC = 512, row = KC * 4; };
-template <> struct FewH<ST_BF16> { static constexpr int KC = 1024, row = KC * 2; };
-template <> struct FewH<ST_FP8> { static constexpr int KC = 2048, row = KC; };
-template <> struct FewH<ST_MX4> { static constexpr int KC = 2048, row = KC; };
-
-__device__ __forceinline__ int32_t take(int32_t* counter)
+// What blocks hand each other (h, expert outputs, counters) is written and read with device-scope accesses, which
+// go past the L2 of the writer's XCD to where every XCD sees them.  A producer's wavefronts wait for their stores
+// before the barrier behind which one lane raises the counter; a consumer's loads come after the barrier behind
+// which that lane has seen it.  (Ordinary stores and a device-scope release instead write back the whole L2 once an
+// item.)
+typedef unsigned long long u64;
+__device__ __forceinline__ void put64(void* p, u64 v) { __hip_atomic_store((u64*)p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ u64 get64(const void* p) { return __hip_atomic_load((u64*)p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); }
+__device__ __forceinline__ uint4 get128(const void* p)
+{
+    const u64 a = get64(p), b = get64((const uint8_t*)p + 8);
+    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
+}
+__device__ __forceinline__ int32_t bump(int32_t* counter)
 {
     return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+// Four consecutive values, rounded to bf16 or as they are.
+template <bool BF> __device__ __forceinline__ void put4(uint8_t* p, const float (&v)[4])
+{
+    if constexpr (BF) {
+        put64(p, (u64)f32x2_to_bf16x2(v[0], v[1]) | (u64)f32x2_to_bf16x2(v[2], v[3]) << 32);
+    } else {
+        put64(p, (u64)__float_as_uint(v[0]) | (u64)__float_as_uint(v[1]) << 32);
+        put64(p + 8, (u64)__float_as_uint(v[2]) | (u64)__float_as_uint(v[3]) << 32);
+    }
+}
 
-template <int ST>
-__global__ __launch_bounds__(64 * FEW_NW) void few_layer_kernel(FewArgs a)
+// Elements of h that a down item keeps in LDS at a time, and the bytes of one as a linear takes it.
+template <int ST> struct FewAct;
+template <> struct FewAct<ST_F32> { static constexpr int bytes = 4, KC = 1024; };
+template <> struct FewAct<ST_BF16> { static constexpr int bytes = 2, KC = 2048; };
+template <> struct FewAct<ST_FP8> { static constexpr int bytes = 1, KC = 4096; };
+template <> struct FewAct<ST_MX4> { static constexpr int bytes = 1, KC = 4096; };
+
+// X_LDS: x fits FEW_XBYTES (rows padded by 16 bytes, so that 16 rows' pieces fall on distinct banks) and is kept in
+// LDS for the up items.
+constexpr int FEW_XBYTES = 16 * (7168 + 16), FEW_XSCALES = 16 * 7168 / 32;
+
+template <int ST, bool X_LDS>
+__global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs a)
 {
     constexpr bool BF = ST != ST_F32;                  // activations are bf16
-    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW;
-    constexpr int KC = FewH<ST>::KC, HSTR = FewH<ST>::row + 16;
-    constexpr int DU = ST == ST_MX4 ? 4 : ST == ST_FP8 ? 3 : 2, DD = ST == ST_MX4 ? 8 : ST == ST_FP8 ? 4 : 2;
-    constexpr int RED = FEW_NW * 2 * 256 * 4, HB = 16 * HSTR;
-    typedef StreamType<ST> TY;
-    __shared__ __attribute__((aligned(16))) uint8_t buf[RED > HB ? RED : HB];   // up: partial sums; down: h
-    __shared__ __attribute__((aligned(16))) uint8_t hsc[16 * (KC / 32)];        // down: scales of the h chunk
+    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K;
+    constexpr int XB = FewAct<ST>::bytes, KC = FewAct<ST>::KC, HSTR = KC * XB + 16;
+    constexpr int DU = !X_LDS ? 5 : ST == ST_FP8 ? 8 : 10, DD = 8;        // units in flight a wavefront: up, down
+    constexpr int HSC = 16 * (KC / 32);
+    constexpr int ACT = X_LDS ? FEW_XBYTES : 16 * HSTR, SC = X_LDS && FEW_XSCALES > HSC ? FEW_XSCALES : HSC;
+    static_assert(KC % (LK * DD) == 0, "a chunk of h is whole rounds of the down product's units");
+    static_assert(16 * HSTR <= ACT && 6 * 1024 <= ACT, "h and the selection's tables fit");
+    __shared__ __attribute__((aligned(16))) uint8_t act[ACT];          // selection's tables; then x; then h
+    __shared__ __attribute__((aligned(16))) uint8_t act_s[SC];         // scales of x; then of h
+    __shared__ __attribute__((aligned(16))) uint8_t tiles[FEW_NW][STREAM_TILE];
     __shared__ int s_idx[FEW_SLOTS];                   // expert of each slot
     __shared__ float s_w[FEW_SLOTS];
-    __shared__ uint16_t s_order[FEW_SLOTS];            // a token's slots by ascending expert
-    __shared__ uint32_t s_tok[1024];                   // tokens (bits) of each expert
-    __shared__ uint16_t s_grp[1024];                   // group of each selected expert
-    __shared__ uint16_t s_exp[FEW_GROUPS], s_n[FEW_GROUPS];
-    __shared__ uint16_t s_slot[FEW_GROUPS][16];        // the slots of a group's rows (group 0: tokens)
+    __shared__ uint8_t s_order[FEW_SLOTS];             // a token's slots by ascending expert
+    __shared__ uint16_t s_exp[FEW_GROUPS];
+    __shared__ uint8_t s_n[FEW_GROUPS];
+    __shared__ uint8_t s_slot[FEW_GROUPS][16];         // the slots of a group's rows (group 0, the shared one: tokens)
     __shared__ int scan[FEW_NW + 1];
     __shared__ int s_item, s_last;
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q = lane >> 4;
     const int T = a.T, k = a.k, E = a.E, d = a.d, slots = T * k;
+    int next = 0;
+    if (tid == 0) next = bump(a.ticket);
 
     // ---- selection: every block for itself
+    uint32_t* s_tok = (uint32_t*)act;                  // tokens (bits) of each expert
+    uint16_t* s_grp = (uint16_t*)(act + 4096);         // group of each selected expert
     for (int e = tid; e < 1024; e += NT) s_tok[e] = 0;
     __syncthreads();
     if (E <= 256) {
@@ -202,29 +256,29 @@ __global__ __launch_bounds__(64 * FEW_NW) void few_layer_kernel(FewArgs a)
         }
     }
     __syncthreads();
+    static_assert(2 * NT == 1024 && 4 * FEW_NW >= FEW_T && NT >= FEW_SLOTS, "two experts a thread, four tokens a wavefront");
     const uint32_t m0 = s_tok[2 * tid], m1 = s_tok[2 * tid + 1];
     int n_sel;
-    const int rank = block_exclusive_scan<NT>((m0 != 0) + (m1 != 0), &n_sel, scan);
-    if (m0) {
-        s_grp[2 * tid] = (uint16_t)(1 + rank);
-        s_exp[1 + rank] = (uint16_t)(2 * tid);
-        s_n[1 + rank] = (uint16_t)__popc(m0);
+    const int rank = 1 + block_exclusive_scan<NT>((m0 != 0) + (m1 != 0), &n_sel, scan);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t m = i ? m1 : m0;
+        const int r = i ? rank + (m0 != 0) : rank;
+        if (m) {
+            s_grp[2 * tid + i] = (uint16_t)r;
+            s_exp[r] = (uint16_t)(2 * tid + i);
+            s_n[r] = (uint8_t)__popc(m);
+        }
     }
-    if (m1) {
-        const int r = 1 + rank + (m0 != 0);
-        s_grp[2 * tid + 1] = (uint16_t)r;
-        s_exp[r] = (uint16_t)(2 * tid + 1);
-        s_n[r] = (uint16_t)__popc(m1);
-    }
-    if (tid < 16) s_slot[0][tid] = (uint16_t)(slots + min(tid, T - 1));
-    if (tid == 0) s_n[0] = (uint16_t)T;
+    if (tid < 16) s_slot[0][tid] = (uint8_t)min(tid, T - 1);
+    if (tid == 0) s_n[0] = (uint8_t)T;
     __syncthreads();
     if (tid < slots) {
         const int t = tid / k, e = s_idx[tid];
-        s_slot[s_grp[e]][__popc(s_tok[e] & ((1u << t) - 1u))] = (uint16_t)tid;
+        s_slot[s_grp[e]][__popc(s_tok[e] & ((1u << t) - 1u))] = (uint8_t)tid;
         int before = 0;
         for (int j = 0; j < k; j++) before += s_idx[t * k + j] < e;
-        s_order[t * k + before] = (uint16_t)tid;
+        s_order[t * k + before] = (uint8_t)tid;
     }
     if (blockIdx.x == 0) {
         if (tid < slots) {
@@ -235,173 +289,168 @@ __global__ __launch_bounds__(64 * FEW_NW) void few_layer_kernel(FewArgs a)
             for (int e = tid; e < E; e += NT) a.counts_out[e] = __popc(s_tok[e]);
     }
     __syncthreads();
+    const int xstr = d * XB + (X_LDS ? 16 : 0);        // bytes between rows of x
+    const int xsstr = ST == ST_MX4 ? d / 32 : ST == ST_FP8 ? d / 128 * 4 : 0;   // ... of its scales
+    if constexpr (X_LDS) {
+        const int vecs = d * XB / 16;                  // 16-byte vectors a row
+        for (int i = tid; i < T * vecs; i += NT) {
+            const int t = i / vecs;
+            *(uint4*)(act + t * xstr + (i - t * vecs) * 16) = ((const uint4*)a.x)[i];
+        }
+        for (int i = tid; i < T * xsstr / 4; i += NT) ((uint32_t*)act_s)[i] = ((const uint32_t*)a.xs)[i];
+        __syncthreads();
+    }
 
     // ---- items
     const int ng = 1 + n_sel, nu_s = a.inter_s / FEW_UP, nu_r = a.inter / FEW_UP, ncol = d / FEW_DN;
-    const int n_up = nu_s + n_sel * nu_r, total = n_up + ng * ncol;
-    int next = 0;
-    if (tid == 0) next = take(a.ticket);
+    const int n_wup = nu_s + n_sel * nu_r;             // wavefront's items of the up products
+    const int n_up = (n_wup + FEW_NW - 1) / FEW_NW, total = n_up + ng * ncol;
     for (;;) {
         if (tid == 0) s_item = next;
         __syncthreads();
-        const int item = s_item;
+        const int item = __builtin_amdgcn_readfirstlane(s_item);
         if (item >= total) break;                      // every block comes to a number past the end
-        if (tid == 0) next = take(a.ticket);           // in flight during the item
+        if (tid == 0) next = bump(a.ticket);           // in flight during the item
 
         if (item < n_up) {
-            // ---- 16 hidden features of one expert: eight wavefronts share K, partial sums joined through LDS
-            const int g = item < nu_s ? 0 : 1 + (item - nu_s) / nu_r;
-            const int f0 = (item < nu_s ? item : (item - nu_s) % nu_r) * FEW_UP;
-            const bool shared = g == 0;
-            const int e = shared ? 0 : s_exp[g], n = s_n[g];
-            const int slot = s_slot[g][r16 < n ? r16 : 0];             // lanes past the rows repeat the first
-            const int64_t tok = slot < slots ? slot / k : slot - slots;
-            const int64_t ldw = (int64_t)(d / 128) * TY::wbytes;
-            const int64_t wrow = (shared ? 0 : (int64_t)e * a.inter) + f0 + r16;
-            const uint8_t* w1 = (shared ? a.S1 : a.W1) + wrow * ldw + 16 * q;
-            const uint8_t* w3 = (shared ? a.S3 : a.W3) + wrow * ldw + 16 * q;
-            const uint8_t *w1s = nullptr, *w3s = nullptr, *as = nullptr;
-            if constexpr (ST == ST_MX4) {
-                w1s = (shared ? a.S1s : a.W1s) + wrow * (d / 32);
-                w3s = (shared ? a.S3s : a.W3s) + wrow * (d / 32);
-                as = a.xs + tok * (d / 32);
-            } else if constexpr (ST == ST_FP8) {
-                const int64_t srow = ((shared ? 0 : (int64_t)e * a.inter) + f0) / 128 * (d / 128) * 4;
-                w1s = (shared ? a.S1s : a.W1s) + srow;
-                w3s = (shared ? a.S3s : a.W3s) + srow;
-                as = a.xs + tok * (d / 128) * 4;
-            }
-            const int nun = d / 128, u0 = nun * wave / FEW_NW, u1 = nun * (wave + 1) / FEW_NW;
-            f32x4 acc1 = {0.f, 0.f, 0.f, 0.f}, acc3 = {0.f, 0.f, 0.f, 0.f};
-            stream_units<ST, true, DU>(acc1, acc3, w1, w1s, w3, w3s, a.x + tok * (d / 128) * TY::abytes + 16 * q, as, u0, u1, q);
-            float* red = (float*)buf;
-            *(f32x4*)(red + wave * 512 + lane * 4) = acc1;
-            *(f32x4*)(red + wave * 512 + 256 + lane * 4) = acc3;
-            __syncthreads();
-            if (tid < 256) {                           // element tid: token (tid / 4) % 16, feature 4 (tid / 64) + tid % 4
-                float gg = 0.f, uu = 0.f;
+            // ---- eight hidden features of one expert a wavefront: eight rows of W1 and the same eight of W3
+            const int it = item * FEW_NW + wave;
+            if (it < n_wup) {
+                const int g = it < nu_s ? 0 : 1 + (it - nu_s) / nu_r;
+                const int f0 = (it < nu_s ? it : (it - nu_s) % nu_r) * FEW_UP;
+                const bool shared = g == 0;
+                const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(s_exp[g]), n = __builtin_amdgcn_readfirstlane(s_n[g]);
+                const int slot = s_slot[g][r16 < n ? r16 : 0];         // lanes past the rows repeat the first
+                const uint32_t tok = shared ? slot : slot / k;
+                const int64_t ldw = (int64_t)d * 128 / LK;
+                const int64_t row0 = (shared ? 0 : (int64_t)e * a.inter) + f0;     // the item's first weight row
+                const uint8_t* s = nullptr;
+                if constexpr (ST == ST_MX4)
+                    s = (shared ? (r16 < 8 ? a.S1s : a.S3s) : (r16 < 8 ? a.W1s : a.W3s)) + (row0 + (r16 & 7)) * (d / 32);
+                if constexpr (ST == ST_FP8)            // the lane's results are of features 4 q .. 4 q + 3
+                    s = (shared ? (q < 2 ? a.S1s : a.S3s) : (q < 2 ? a.W1s : a.W3s)) + row0 / 128 * (d / 128) * 4;
+                const WRows wr = weight_rows<ST>((shared ? a.S1 : a.W1) + row0 * ldw, (shared ? a.S3 : a.W3) + row0 * ldw, s, ldw, d, lane);
+                const ARows ax = {X_LDS ? act : a.x, X_LDS ? act_s : a.xs, tok * xstr + 16 * q, tok * xsstr, wr.half};
+                const int nu = stream_units_of<ST>(d);
+                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+                Stream<ST, X_LDS, DU> st;
+                st.begin(wr, ax, nu);
+                st.run(acc, ax, 0, nu, nu, tiles[wave], lane);
+                // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
+                float hv[4];
 #pragma unroll
-                for (int w = 0; w < FEW_NW; w++) {
-                    gg += red[w * 512 + tid];
-                    uu += red[w * 512 + 256 + tid];
+                for (int r = 0; r < 4; r++) {
+                    float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
+                    if constexpr (BF) {
+                        round_bf16x2(gg, uu);
+                        hv[r] = silu_mul_fast(gg, uu);
+                    } else {
+                        hv[r] = silu_mul(gg, uu);
+                    }
                 }
-                const int r = (tid >> 2) & 15, f = f0 + 4 * (tid >> 6) + (tid & 3);
-                if constexpr (BF) {
-                    round_bf16x2(gg, uu);
-                    if (r < n) ((uint16_t*)a.h)[(int64_t)s_slot[g][r] * a.inter_max + f] = f32_to_bf16(silu_mul_fast(gg, uu));
-                } else {
-                    if (r < n) ((float*)a.h)[(int64_t)s_slot[g][r] * a.inter_max + f] = silu_mul(gg, uu);
+                if (q < 2 && r16 < n) {
+                    const int64_t hrow = shared ? slots + slot : slot;
+                    put4<BF>(a.h + (hrow * a.inter_max + f0 + 4 * q) * AB, hv);
                 }
+                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+                if (lane == 0) bump(&a.up_done[g * FEW_PAD]);
             }
             __syncthreads();
-            if (tid == 0) __hip_atomic_fetch_add(&a.up_done[g], 1, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
             continue;
         }
 
-        // ---- 128 output features of one expert: a wavefront takes 16 of them over the whole K
+        // ---- 16 output features of one expert a wavefront, over the whole K
         const int v = item - n_up, g = v / ncol, c = v % ncol;
         const bool shared = g == 0;
-        const int e = shared ? 0 : s_exp[g], n = s_n[g], K = shared ? a.inter_s : a.inter;
-        const int64_t ldw = (int64_t)(K / 128) * TY::wbytes;
-        const int64_t wrow = (shared ? 0 : (int64_t)e * d) + c * FEW_DN + wave * 16 + r16;
-        const uint8_t* w2 = (shared ? a.S2 : a.W2) + wrow * ldw + 16 * q;
-        const uint8_t* w2s = nullptr;
-        if constexpr (ST == ST_MX4) w2s = (shared ? a.S2s : a.W2s) + wrow * (K / 32);
-        else if constexpr (ST == ST_FP8)
-            w2s = (shared ? a.S2s : a.W2s) + ((shared ? 0 : (int64_t)e * d) + c * FEW_DN + wave * 16) / 128 * (K / 128) * 4;
-        const int nun = K / 128;
-        WUnit<ST> rw[DD];
-#pragma unroll
-        for (int j = 0; j < DD; j++) rw[j].load(w2, w2s, min(j, nun - 1));      // these need no h
+        const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(s_exp[g]), n = __builtin_amdgcn_readfirstlane(s_n[g]), K = shared ? a.inter_s : a.inter;
+        const int64_t ldw = (int64_t)K * 128 / LK;
+        const int64_t row0 = (shared ? 0 : (int64_t)e * d) + c * FEW_DN + wave * 16;   // the wavefront's first row
+        const uint8_t* s = nullptr;
+        if constexpr (ST == ST_MX4) s = (shared ? a.S2s : a.W2s) + (row0 + r16) * (K / 32);
+        if constexpr (ST == ST_FP8) s = (shared ? a.S2s : a.W2s) + row0 / 128 * (K / 128) * 4;
+        const uint8_t* p0 = (shared ? a.S2 : a.W2) + row0 * ldw;
+        const WRows wr = weight_rows<ST>(p0, p0 + 8 * ldw, s, ldw, K, lane);
+        const int nu = stream_units_of<ST>(K);
+        Stream<ST, true, DD> st;
+        st.begin(wr, {}, nu);                          // these need no h
         if (tid == 0) {
             const int need = shared ? nu_s : nu_r;
-            while (__hip_atomic_load(&a.up_done[g], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
-                __builtin_amdgcn_s_sleep(1);
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+            while (__hip_atomic_load(&a.up_done[g * FEW_PAD], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
+                __builtin_amdgcn_s_sleep(8);
         }
         __syncthreads();
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         const int ar = r16 < n ? r16 : 0;
-        for (int u0 = 0; u0 < nun; u0 += KC / 128) {
-            const int kc = min(KC, K - u0 * 128);      // elements of this chunk
-            if (u0) __syncthreads();                   // the chunk before is used up
+        for (int k0 = 0; k0 < K; k0 += KC) {
+            const int kc = min(KC, K - k0);            // elements of this chunk
+            if (k0) __syncthreads();                   // the chunk before is used up
             const int vecs = kc / 8;                   // 8 elements a thread; a multiple of 16
             for (int i = tid; i < n * vecs; i += NT) {
-                const int r = i / vecs, p = i % vecs;
-                const int64_t src = (int64_t)s_slot[g][r] * a.inter_max + u0 * 128 + p * 8;
+                const int r = i / vecs, p = i - r * vecs, sl = s_slot[g][r];
+                const uint8_t* src = a.h + ((int64_t)(shared ? slots + sl : sl) * a.inter_max + k0 + p * 8) * AB;
+                uint8_t* dst = act + r * HSTR;
                 if constexpr (ST == ST_F32) {
-                    const float4* s = (const float4*)((const float*)a.h + src);
-                    *(float4*)(buf + r * HSTR + p * 32) = s[0];
-                    *(float4*)(buf + r * HSTR + p * 32 + 16) = s[1];
+                    *(uint4*)(dst + p * 32) = get128(src);
+                    *(uint4*)(dst + p * 32 + 16) = get128(src + 16);
                 } else {
-                    const uint4 raw = *(const uint4*)((const uint16_t*)a.h + src);
+                    const uint4 raw = get128(src);
                     if constexpr (ST == ST_BF16) {
-                        *(uint4*)(buf + r * HSTR + p * 16) = raw;
+                        *(uint4*)(dst + p * 16) = raw;
                     } else {
                         float hv[8];
                         bf16x8_to_f32(raw, hv);
                         if constexpr (ST == ST_MX4) {
                             const uint32_t sc = mx_scale_code<false>(quad_max(mx_amax8(hv)));
-                            *(uint2*)(buf + r * HSTR + p * 8) = sc == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(hv, sc);
-                            if ((p & 3) == 0) hsc[r * (KC / 32) + p / 4] = (uint8_t)sc;
+                            *(uint2*)(dst + p * 8) = sc == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(hv, sc);
+                            if ((p & 3) == 0) act_s[r * (KC / 32) + p / 4] = (uint8_t)sc;
                         } else {
                             float sc;
-                            *(uint2*)(buf + r * HSTR + p * 8) = quant8_e4m3(hv, sc);
-                            if ((p & 15) == 0) ((float*)hsc)[r * (KC / 128) + p / 16] = sc;
+                            *(uint2*)(dst + p * 8) = quant8_e4m3(hv, sc);
+                            if ((p & 15) == 0) ((float*)act_s)[r * (KC / 128) + p / 16] = sc;
                         }
                     }
                 }
             }
             __syncthreads();
-            const uint8_t* hb = buf + ar * HSTR + 16 * q;
-            const uint8_t* hs = hsc + ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4);
-            for (int u = 0; u < kc / 128; u += DD) {
-#pragma unroll
-                for (int j = 0; j < DD; j++) {
-                    if (u + j < kc / 128) {
-                        AUnit<ST> ra;
-                        ra.load(hb, hs, u + j);
-                        stream_mma<ST>(acc, rw[j], ra, q);
-                        rw[j].load(w2, w2s, min(u0 + u + j + DD, nun - 1));
-                    }
-                }
-            }
+            const ARows hrow = {act, act_s, (uint32_t)(ar * HSTR + 16 * q),
+                                (uint32_t)(ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4)), ST == ST_MX4 && kc % 256 ? kc / 256 : -1};
+            st.run(acc, hrow, k0 / LK, k0 / LK + stream_units_of<ST>(kc), nu, tiles[wave], lane);
         }
         // this lane: features 4 q .. 4 q + 3 of the group's row r16
         if (r16 < n) {
-            uint8_t* o = a.y_rows + ((int64_t)s_slot[g][r16] * d + c * FEW_DN + wave * 16 + 4 * q) * AB;
-            if constexpr (BF) *(uint2*)o = make_uint2(f32x2_to_bf16x2(acc[0], acc[1]), f32x2_to_bf16x2(acc[2], acc[3]));
-            else *(f32x4*)o = acc;
+            const int sl = s_slot[g][r16];
+            const float o[4] = {acc[0], acc[1], acc[2], acc[3]};
+            put4<BF>(a.y_rows + ((int64_t)(shared ? slots + sl : sl) * d + c * FEW_DN + wave * 16 + 4 * q) * AB, o);
         }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         __syncthreads();
-        if (tid == 0)
-            s_last = __hip_atomic_fetch_add(&a.col_done[c], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == ng - 1;
+        if (tid == 0) s_last = bump(&a.col_done[c * FEW_PAD]) == ng - 1;
         __syncthreads();
         if (s_last) {
             // the experts' outputs for these columns are there: the combine, by ascending expert, then the shared one
-            __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-            constexpr int VE = 16 / AB, VR = FEW_DN / VE;              // elements of a vector, vectors of a row
+            constexpr int VE = 16 / AB;                // elements of a vector
+            constexpr int VR = FEW_DN / VE;            // vectors of a row
             for (int i = tid; i < T * VR; i += NT) {
                 const int t = i / VR;
                 const int64_t col = c * FEW_DN + i % VR * VE;
-                float s[VE];
+                float sum[VE];
 #pragma unroll
-                for (int j = 0; j < VE; j++) s[j] = 0.f;
+                for (int j = 0; j < VE; j++) sum[j] = 0.f;
                 for (int j = 0; j <= k; j++) {
                     const int sl = j < k ? s_order[t * k + j] : slots + t;
-                    const uint4 raw = *(const uint4*)(a.y_rows + ((int64_t)sl * d + col) * AB);
+                    const uint4 raw = get128(a.y_rows + ((int64_t)sl * d + col) * AB);
                     const uint32_t wv[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
                     for (int m = 0; m < VE; m++) {
                         const float o = BF ? __uint_as_float(m & 1 ? (wv[m / 2] & 0xFFFF0000u) : (wv[m / 2] << 16))
                                            : __uint_as_float(wv[m]);
-                        s[m] = j < k ? s[m] + o * s_w[sl] : s[m] + o;
+                        sum[m] = j < k ? sum[m] + o * s_w[sl] : sum[m] + o;
                     }
                 }
                 uint4 o;
-                if constexpr (BF) o = make_uint4(f32x2_to_bf16x2(s[0], s[1]), f32x2_to_bf16x2(s[2], s[3]),
-                                                 f32x2_to_bf16x2(s[4], s[5]), f32x2_to_bf16x2(s[6], s[7]));
-                else o = make_uint4(__float_as_uint(s[0]), __float_as_uint(s[1]), __float_as_uint(s[2]), __float_as_uint(s[3]));
+                if constexpr (BF) o = make_uint4(f32x2_to_bf16x2(sum[0], sum[1]), f32x2_to_bf16x2(sum[2], sum[3]),
+                                                 f32x2_to_bf16x2(sum[4], sum[5]), f32x2_to_bf16x2(sum[6], sum[7]));
+                else o = make_uint4(__float_as_uint(sum[0]), __float_as_uint(sum[1]), __float_as_uint(sum[2]), __float_as_uint(sum[3]));
                 *(uint4*)(a.y + ((int64_t)t * d + col) * AB) = o;
             }
         }
@@ -430,7 +479,7 @@ static FewWorkspace carve_few(const moe_shape_t& s, void* base)
         off += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    w.n_counters = 1 + FEW_GROUPS + (int)(d / FEW_DN);
+    w.n_counters = (1 + FEW_GROUPS + (int)(d / FEW_DN)) * FEW_PAD;
     w.counters = (int32_t*)take_bytes(4 * (size_t)w.n_counters);
     w.logits = (float*)take_bytes(4 * T * (size_t)s.E);
     if (s.w_dtype == MOE_FP8_E4M3 || s.w_dtype == MOE_MXFP4) {
@@ -450,8 +499,8 @@ static void launch_prepare(const moe_shape_t& s, const void* x, const float* Wg,
                            hipStream_t stream)
 {
     const bool quant = ST == ST_FP8 || ST == ST_MX4;
-    const int nq = quant ? (int)((s.T * s.d / 8 + 255) / 256) : 0;
-    few_prepare_kernel<ST, TM><<<(unsigned)(s.E + nq + 1), 256, 0, stream>>>(x, Wg, bias, w.logits, (int)s.T, (int)s.d, (int)s.E,
+    const int nq = quant ? (int)((s.T * s.d / 8 + FEW_NT1 - 1) / FEW_NT1) : 0;
+    few_prepare_kernel<ST, TM><<<(unsigned)(s.E + nq + 1), FEW_NT1, 0, stream>>>(x, Wg, bias, w.logits, (int)s.T, (int)s.d, (int)s.E,
                                                                              w.xq, w.xs, w.counters, w.n_counters);
 }
 
@@ -466,8 +515,10 @@ static hipError_t launch_few_t(const moe_shape_t& s, const void* x, const float*
     else launch_prepare<ST, 16>(s, x, Wg, bias, w, stream);
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
-    // two blocks for each of the card's 256 CUs (any number is right: see above)
-    few_layer_kernel<ST><<<512, 64 * FEW_NW, 0, stream>>>(a);
+    // a block for each of the card's 256 CUs (any number is right: see above)
+    const int64_t row = s.d * FewAct<ST>::bytes + 16;
+    if (s.T * row <= FEW_XBYTES && s.T * s.d / 32 <= FEW_XSCALES) few_layer_kernel<ST, true><<<256, 64 * FEW_NW, 0, stream>>>(a);
+    else few_layer_kernel<ST, false><<<256, 64 * FEW_NW, 0, stream>>>(a);
     return hipGetLastError();
 }
 
@@ -506,8 +557,8 @@ hipError_t launch_few(const moe_shape_t& s, const void* x, const float* Wg, cons
     a.w_out_bits = (int32_t*)w_out;
     a.counts_out = counts_out;
     a.ticket = w.counters;
-    a.up_done = w.counters + 1;
-    a.col_done = w.counters + 1 + FEW_GROUPS;
+    a.up_done = w.counters + FEW_PAD;
+    a.col_done = w.counters + (1 + FEW_GROUPS) * FEW_PAD;
     if (s.act_dtype == MOE_F32) return launch_few_t<ST_F32>(s, x, Wg, bias, a, w, stream);
     if (s.w_dtype == MOE_FP8_E4M3) return launch_few_t<ST_FP8>(s, x, Wg, bias, a, w, stream);
     if (s.w_dtype == MOE_MXFP4) return launch_few_t<ST_MX4>(s, x, Wg, bias, a, w, stream);

@@ -34,14 +34,20 @@ template <bool UP> __device__ __forceinline__ MxGroup mx_group(const GemmArgs& g
 }
 
 // ---------------------------------------------------------------------------------------------------
-// 16-row tiles (decode): a block is one tile x 128 output features, eight wavefronts of 16 features, each
-// streaming its weight rows over the whole K.  Weight bytes bound it.
+// 16-row tiles (decode): weight bytes bound it.  A block is one tile x 256 output features for the down GEMM, 128
+// for the up GEMM; each of its 16 wavefronts streams 16 weight rows (up: eight of W1 and the same eight of W3) over
+// the whole K, the tile's activation rows in LDS (up to XK elements of K at a time).
 // ---------------------------------------------------------------------------------------------------
 template <bool UP>
-__global__ __launch_bounds__(512) void mx_gemm_stream_kernel(GemmArgs g)
+__global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
 {
-    constexpr int BN = 128, D = 4;
-    __shared__ __attribute__((aligned(16))) float hs[16][BN + 4];
+    constexpr int NW = 16, NT = 64 * NW, FW = UP ? 8 : 16, BN = NW * FW, D = 4;
+    constexpr int XK = UP ? 7168 : 4096, XSTR = XK + 16;               // whole rounds of D units
+    static_assert(XK % (D * 256) == 0, "a chunk of K is whole rounds");
+    __shared__ __attribute__((aligned(16))) uint8_t xb[16 * XSTR];
+    __shared__ __attribute__((aligned(16))) uint8_t xs[16 * (XK / 32)];
+    __shared__ __attribute__((aligned(16))) uint8_t tiles[NW][STREAM_TILE];
+    static_assert(16 * (BN + 4) * 4 <= NW * STREAM_TILE, "the output tile replaces the weight tiles");
 
     int tile, nb;
     if (!block_work(g, tile, nb)) return;
@@ -51,34 +57,62 @@ __global__ __launch_bounds__(512) void mx_gemm_stream_kernel(GemmArgs g)
     const int N = shared ? g.N_s : g.N_r, K = shared ? g.K_s : g.K_r;
     const int n0 = nb * BN;
     if (n0 >= N) return;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q = lane >> 4;
     const MxGroup m = mx_group<UP>(g, grp, shared, N, K);
 
-    // lanes past the tile's rows repeat its first row (valid memory; computed, never stored)
-    const int ar = row0 + (r16 < rows ? r16 : 0);
-    const int64_t arow = UP ? g.row_token[ar] : ar;
-    const int64_t wrow = n0 + wave * 16 + r16;
-    f32x4 acc1 = {0.f, 0.f, 0.f, 0.f}, acc3 = {0.f, 0.f, 0.f, 0.f};
-    stream_units<ST_MX4, UP, D>(acc1, acc3, m.W1 + wrow * m.ldb + 16 * q, m.W1s + wrow * m.nkb, m.W3 + wrow * m.ldb + 16 * q,
-                                m.W3s + wrow * m.nkb, g.A + arow * g.lda + 16 * q, bytes(g.As) + arow * g.ldas, 0, K / 128, q);
+    // N is a multiple of 128: the down GEMM's last block may be half there (its other wavefronts repeat the first)
+    const bool mine = n0 + wave * FW < N;
+    const int64_t w0 = mine ? n0 + wave * FW : n0;     // the wavefront's first feature
+    const uint8_t* p0 = m.W1 + w0 * m.ldb;
+    const uint8_t* s = UP ? (r16 < 8 ? m.W1s : m.W3s) + (w0 + (r16 & 7)) * m.nkb : m.W1s + (w0 + r16) * m.nkb;
+    const WRows wr = weight_rows<ST_MX4>(p0, UP ? m.W3 + w0 * m.ldb : p0 + 8 * m.ldb, s, m.ldb, K, lane);
+    const int nu = stream_units_of<ST_MX4>(K);
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    Stream<ST_MX4, true, D> st;
+    for (int k0 = 0; k0 < K; k0 += XK) {
+        const int kc = min(XK, K - k0), vecs = kc / 16;
+        if (k0) __syncthreads();                       // the chunk before is used up
+        for (int i = tid; i < rows * vecs; i += NT) {
+            const int r = i / vecs, p = i - r * vecs;
+            const int64_t arow = UP ? g.row_token[row0 + r] : row0 + r;
+            *(uint4*)(xb + r * XSTR + p * 16) = *(const uint4*)(g.A + arow * g.lda + k0 + p * 16);
+        }
+        for (int i = tid; i < rows * (kc / 128); i += NT) {
+            const int r = i / (kc / 128), p = i - r * (kc / 128);
+            const int64_t arow = UP ? g.row_token[row0 + r] : row0 + r;
+            *(uint32_t*)(xs + r * (XK / 32) + p * 4) = *(const uint32_t*)(bytes(g.As) + arow * g.ldas + k0 / 32 + p * 4);
+        }
+        if (k0 == 0) st.begin(wr, {}, nu);             // behind the activations' loads, so that these do not wait for it
+        lds_barrier();
+        const int ar = r16 < rows ? r16 : 0;           // lanes past the tile's rows repeat its first row (never stored)
+        const ARows a = {xb, xs, (uint32_t)(ar * XSTR + 16 * q), (uint32_t)(ar * (XK / 32)), kc % 256 ? kc / 256 : -1};
+        st.run(acc, a, k0 / 256, k0 / 256 + stream_units_of<ST_MX4>(kc), nu, tiles[wave], lane);
+    }
+    __syncthreads();
 
-    // [token][feature] through LDS, then whole 16-lane rows: h quantised per 32 features, or y rounded to bf16
+    // [token][feature] through LDS, then whole rows: h quantised per 32 features, or y rounded to bf16
+    float* hs = (float*)tiles;                         // [16][BN + 4]
     if constexpr (UP) {
+        // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
 #pragma unroll
         for (int r = 0; r < 4; r++) {
-            float gg = acc1[r], uu = acc3[r];
+            float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
             round_bf16x2(gg, uu);
-            acc1[r] = round_bf16(silu_mul_fast(gg, uu));
+            acc[r] = round_bf16(silu_mul_fast(gg, uu));
         }
+        if (q < 2) *(f32x4*)(hs + r16 * (BN + 4) + wave * 8 + 4 * q) = acc;
+    } else {
+        *(f32x4*)(hs + r16 * (BN + 4) + wave * 16 + 4 * q) = acc;
     }
-    *(f32x4*)&hs[r16][wave * 16 + 4 * q] = acc1;
     __syncthreads();
-    const int row = tid >> 4, sub = tid & 15;          // 16 threads a row, 8 features each
-    if (row < rows) {                                  // rows <= 16: the block's first four wavefronts
+    constexpr int TR = BN / 8;                         // threads a row, 8 features each
+    const int row = tid / TR, sub = tid % TR;
+    if (row < rows && n0 + sub * 8 < N) {              // rows <= 16
         float v[8];
-        *(f32x4*)&v[0] = *(const f32x4*)&hs[row][sub * 8];
-        *(f32x4*)&v[4] = *(const f32x4*)&hs[row][sub * 8 + 4];
+        *(f32x4*)&v[0] = *(const f32x4*)(hs + row * (BN + 4) + sub * 8);
+        *(f32x4*)&v[4] = *(const f32x4*)(hs + row * (BN + 4) + sub * 8 + 4);
         const int64_t orow = (int64_t)row0 + row;
         if constexpr (UP) {
             const uint32_t c = mx_scale_code<false>(quad_max(mx_amax8(v)));
@@ -292,9 +326,9 @@ static void launch_mx(const moe_shape_t& s, GemmArgs a, int N, hipStream_t strea
 {
     const int bm = tile_rows(s);
     const bool wide = !UP && N % 256 == 0;             // down: 256-wide n-blocks where d allows
-    a.n_blocks = N / (bm > 16 && wide ? 256 : 128);
+    a.n_blocks = bm == 16 && !UP ? (N + 255) / 256 : N / (wide ? 256 : 128);
     const unsigned grid = (unsigned)launch_blocks(a);
-    if (bm == 16) mx_gemm_stream_kernel<UP><<<grid, 512, 0, stream>>>(a);
+    if (bm == 16) mx_gemm_stream_kernel<UP><<<grid, 1024, 0, stream>>>(a);
     else if constexpr (UP) {
         if (bm == 128) mx_gemm_kernel<true, 128, 128, 4><<<grid, 512, 0, stream>>>(a);
         else mx_gemm_kernel<true, 256, 128, 3><<<grid, 512, 0, stream>>>(a);
