@@ -7,17 +7,18 @@
 //     weight type has one; the counters of launch 2 set to zero.
 //   launch 2 (few_layer_kernel): a grid that fills the card once, whose blocks take work items from one counter
 //     until none is left.  Every block first selects the experts itself (a top-k over T rows of logits, cheaper
-//     than a hand-off between blocks).  Items, in this order: the up products of the shared expert and of each
-//     selected expert, 16 hidden features an item; then their down products, 128 output features an item.  A
-//     down item waits for its expert's up items, and the block that completes the last down item of a column
-//     range sums the experts' outputs there.  No launch boundary lies between the phases: blocks stream down
-//     weights while others finish up items.
+//     than a hand-off between blocks) and keeps x in LDS where it fits.  Items, in this order: the up products of the
+//     shared expert and of each selected expert, eight hidden features a wavefront; then their down products, 32
+//     output features a wavefront.  A down item waits for its expert's up items, its first weights on their way
+//     meanwhile, and the block that completes the last down item of a column range sums the experts' outputs there.
+//     No launch boundary lies between the phases.
 //
 // Why every wait ends.  Blocks take item numbers from the counter in ascending order, and an item waits only for
 // items of lower numbers.  Take the lowest unfinished item: the block that holds it is running (it took the
-// number) and has finished what it held before, since that has a lower number; what the item waits for is
-// finished too; so it completes.  This holds for any number of resident blocks, in any order of dispatch, and
-// beside other kernels (a second call of this one among them).
+// number), and what it held before is finished or under way without a wait, since that has a lower number; what the
+// item waits for is finished too; so it completes.  This holds for any number of resident blocks, in any order of
+// dispatch, and beside other kernels (a second call of this one among them).  Inside a block, wavefronts wait for
+// the number that the first one leaves in LDS; it does so before it waits for anything itself.
 //
 // Router logits.  The products x[t][i] * Wg[e][i] are exact in fp64 and are summed there, the bias is added, and
 // the sum is rounded once to fp32: over a row of 2^13 terms fp64's error is below 2^-40 of the terms' magnitudes,
@@ -57,7 +58,7 @@ struct FewArgs {
 // Launch 1.  Blocks [0, E): the logits of one expert for every token.  Blocks [E, E + nq): quantisation of x.
 // The last block clears the counters.
 // ---------------------------------------------------------------------------------------------------
-constexpr int FEW_NT1 = 512;                           // threads per block of launch 1
+constexpr int FEW_NT1 = 1024;                          // threads per block of launch 1
 
 template <typename XT> __device__ __forceinline__ void load4(const XT* p, double (&v)[4]);
 template <> __device__ __forceinline__ void load4<uint16_t>(const uint16_t* p, double (&v)[4])
@@ -185,30 +186,36 @@ template <bool BF> __device__ __forceinline__ void put4(uint8_t* p, const float 
     }
 }
 
-// Elements of h that a down item keeps in LDS at a time, and the bytes of one as a linear takes it.
-template <int ST> struct FewAct;
-template <> struct FewAct<ST_F32> { static constexpr int bytes = 4, KC = 1024; };
-template <> struct FewAct<ST_BF16> { static constexpr int bytes = 2, KC = 2048; };
-template <> struct FewAct<ST_FP8> { static constexpr int bytes = 1, KC = 4096; };
-template <> struct FewAct<ST_MX4> { static constexpr int bytes = 1, KC = 4096; };
+// The kernel's argument block (its only argument).
+typedef const __attribute__((address_space(4))) FewArgs* KernArgs;
 
-// X_LDS: x fits FEW_XBYTES (rows padded by 16 bytes, so that 16 rows' pieces fall on distinct banks) and is kept in
-// LDS for the up items.
-constexpr int FEW_XBYTES = 16 * (7168 + 16), FEW_XSCALES = 16 * 7168 / 32;
+// Bytes of an activation as a linear takes it, and the elements of h that fit LDS at a time.
+template <int ST> struct FewAct;
+template <> struct FewAct<ST_F32> { static constexpr int bytes = 4; };
+template <> struct FewAct<ST_BF16> { static constexpr int bytes = 2; };
+template <> struct FewAct<ST_FP8> { static constexpr int bytes = 1; };
+template <> struct FewAct<ST_MX4> { static constexpr int bytes = 1; };
+
+// LDS for activations: 16 rows of up to 7168 bytes, each padded by 16 so that 16 rows' pieces fall on distinct banks.
+// X_LDS: x fits (rows of d elements) and is kept there for the up items.
+constexpr int FEW_ROW = 7168, FEW_XBYTES = 16 * (FEW_ROW + 16), FEW_XSCALES = 16 * FEW_ROW / 32;
+
+// What a wavefront does next.
+struct FewJob {
+    int kind, g, at;                                   // group; first hidden feature (up) or column range (down)
+};
+enum { FEW_NONE = 0, FEW_IDLE = 1, FEW_UP_JOB = 2, FEW_DN_JOB = 3 };
 
 template <int ST, bool X_LDS>
-__global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs a)
+__global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
 {
     constexpr bool BF = ST != ST_F32;                  // activations are bf16
-    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K;
-    constexpr int XB = FewAct<ST>::bytes, KC = FewAct<ST>::KC, HSTR = KC * XB + 16;
-    constexpr int DU = !X_LDS ? 5 : ST == ST_FP8 ? 8 : 10, DD = 8;        // units in flight a wavefront: up, down
-    constexpr int HSC = 16 * (KC / 32);
-    constexpr int ACT = X_LDS ? FEW_XBYTES : 16 * HSTR, SC = X_LDS && FEW_XSCALES > HSC ? FEW_XSCALES : HSC;
-    static_assert(KC % (LK * DD) == 0, "a chunk of h is whole rounds of the down product's units");
-    static_assert(16 * HSTR <= ACT && 6 * 1024 <= ACT, "h and the selection's tables fit");
-    __shared__ __attribute__((aligned(16))) uint8_t act[ACT];          // selection's tables; then x; then h
-    __shared__ __attribute__((aligned(16))) uint8_t act_s[SC];         // scales of x; then of h
+    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = 8;
+    constexpr int XB = FewAct<ST>::bytes, HSTR = FEW_ROW + 16;
+    constexpr int KC = FEW_ROW / XB / (LK * D) * (LK * D);             // elements of h in LDS at a time: whole rounds
+    static_assert(KC > 0, "a round of h fits a row");
+    __shared__ __attribute__((aligned(16))) uint8_t act[FEW_XBYTES];   // x; then h
+    __shared__ __attribute__((aligned(16))) uint8_t act_s[FEW_XSCALES];        // their scales
     __shared__ __attribute__((aligned(16))) uint8_t tiles[FEW_NW][STREAM_TILE];
     __shared__ int s_idx[FEW_SLOTS];                   // expert of each slot
     __shared__ float s_w[FEW_SLOTS];
@@ -216,47 +223,46 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs a)
     __shared__ uint16_t s_exp[FEW_GROUPS];
     __shared__ uint8_t s_n[FEW_GROUPS];
     __shared__ uint8_t s_slot[FEW_GROUPS][16];         // the slots of a group's rows (group 0, the shared one: tokens)
+    __shared__ volatile uint64_t s_ticket[64];         // round + 1 and the item number taken for it, by round % 64
     __shared__ int scan[FEW_NW + 1];
-    __shared__ int s_item, s_last;
+    __shared__ int s_last;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q = lane >> 4;
-    const int T = a.T, k = a.k, E = a.E, d = a.d, slots = T * k;
-    int next = 0;
-    if (tid == 0) next = bump(a.ticket);
+    const int T = args.T, k = args.k, E = args.E, d = args.d, slots = T * k;
+    const int xstr = d * XB + (X_LDS ? 16 : 0);        // bytes between rows of x
+    const int xsstr = ST == ST_MX4 ? d / 32 : ST == ST_FP8 ? d / 128 * 4 : 0;   // ... of its scales
+    int ticket = 0;
+    if (tid == 0) ticket = bump(args.ticket);
 
-    // ---- selection: every block for itself
-    uint32_t* s_tok = (uint32_t*)act;                  // tokens (bits) of each expert
-    uint16_t* s_grp = (uint16_t*)(act + 4096);         // group of each selected expert
-    for (int e = tid; e < 1024; e += NT) s_tok[e] = 0;
-    __syncthreads();
-    if (E <= 256) {
-        if (wave * 4 < T) {                            // wavefront-uniform
-            const int t = wave * 4 + q;
-            int e;
-            float w;
-            topk_group<16, 16>(a.logits + (size_t)min(t, T - 1) * E, nullptr, E, k, r16, e, w);
-            if (t < T && r16 < k) {
-                s_idx[t * k + r16] = e;
-                s_w[t * k + r16] = w;
-                atomicOr(&s_tok[e], 1u << t);
-            }
+    // ---- x into LDS, and the selection: every block for itself
+    if constexpr (X_LDS) {
+        const int vecs = d * XB / 16;                  // 16-byte vectors a row
+        for (int i = tid; i < T * vecs; i += NT) {
+            const int t = i / vecs;
+            *(uint4*)(act + t * xstr + (i - t * vecs) * 16) = ((const uint4*)args.x)[i];
         }
-    } else {
-        for (int t = wave; t < T; t += FEW_NW) {
-            int e;
-            float w;
-            topk_group<64, 16>(a.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
-            if (lane < k) {
-                s_idx[t * k + lane] = e;
-                s_w[t * k + lane] = w;
-                atomicOr(&s_tok[e], 1u << t);
-            }
+        for (int i = tid; i < T * xsstr / 4; i += NT) ((uint32_t*)act_s)[i] = ((const uint32_t*)args.xs)[i];
+    }
+    uint32_t* s_tok = (uint32_t*)tiles;                // tokens (bits) of each expert
+    uint16_t* s_grp = (uint16_t*)(s_tok + 1024);       // group of each selected expert
+    if (tid < 64) s_ticket[tid] = 0;
+    s_tok[tid] = s_tok[NT + tid] = 0;
+    __syncthreads();
+    static_assert(2 * NT == 1024 && NT >= FEW_SLOTS, "two experts a thread, a slot a thread");
+    for (int t = wave; t < T; t += FEW_NW) {
+        int e;
+        float w;
+        if (E <= 256) topk_group<64, 4>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
+        else topk_group<64, 16>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
+        if (lane < k) {
+            s_idx[t * k + lane] = e;
+            s_w[t * k + lane] = w;
+            atomicOr(&s_tok[e], 1u << t);
         }
     }
     __syncthreads();
-    static_assert(2 * NT == 1024 && 4 * FEW_NW >= FEW_T && NT >= FEW_SLOTS, "two experts a thread, four tokens a wavefront");
     const uint32_t m0 = s_tok[2 * tid], m1 = s_tok[2 * tid + 1];
     int n_sel;
     const int rank = 1 + block_exclusive_scan<NT>((m0 != 0) + (m1 != 0), &n_sel, scan);
@@ -282,157 +288,107 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs a)
     }
     if (blockIdx.x == 0) {
         if (tid < slots) {
-            if (a.idx_out) a.idx_out[tid] = s_idx[tid];
-            if (a.w_out_bits) a.w_out_bits[tid] = __float_as_int(s_w[tid]);
+            if (args.idx_out) args.idx_out[tid] = s_idx[tid];
+            if (args.w_out_bits) args.w_out_bits[tid] = __float_as_int(s_w[tid]);
         }
-        if (a.counts_out)
-            for (int e = tid; e < E; e += NT) a.counts_out[e] = __popc(s_tok[e]);
+        if (args.counts_out)
+            for (int e = tid; e < E; e += NT) args.counts_out[e] = __popc(s_tok[e]);
     }
+    if (tid == 0) s_ticket[0] = 1ull << 32 | (uint32_t)ticket;
     __syncthreads();
-    const int xstr = d * XB + (X_LDS ? 16 : 0);        // bytes between rows of x
-    const int xsstr = ST == ST_MX4 ? d / 32 : ST == ST_FP8 ? d / 128 * 4 : 0;   // ... of its scales
-    if constexpr (X_LDS) {
-        const int vecs = d * XB / 16;                  // 16-byte vectors a row
-        for (int i = tid; i < T * vecs; i += NT) {
-            const int t = i / vecs;
-            *(uint4*)(act + t * xstr + (i - t * vecs) * 16) = ((const uint4*)a.x)[i];
-        }
-        for (int i = tid; i < T * xsstr / 4; i += NT) ((uint32_t*)act_s)[i] = ((const uint32_t*)a.xs)[i];
-        __syncthreads();
-    }
 
-    // ---- items
-    const int ng = 1 + n_sel, nu_s = a.inter_s / FEW_UP, nu_r = a.inter / FEW_UP, ncol = d / FEW_DN;
-    const int n_wup = nu_s + n_sel * nu_r;             // wavefront's items of the up products
-    const int n_up = (n_wup + FEW_NW - 1) / FEW_NW, total = n_up + ng * ncol;
-    for (;;) {
-        if (tid == 0) s_item = next;
-        __syncthreads();
-        const int item = __builtin_amdgcn_readfirstlane(s_item);
-        if (item >= total) break;                      // every block comes to a number past the end
-        if (tid == 0) next = bump(a.ticket);           // in flight during the item
-
-        if (item < n_up) {
-            // ---- eight hidden features of one expert a wavefront: eight rows of W1 and the same eight of W3
-            const int it = item * FEW_NW + wave;
-            if (it < n_wup) {
-                const int g = it < nu_s ? 0 : 1 + (it - nu_s) / nu_r;
-                const int f0 = (it < nu_s ? it : (it - nu_s) % nu_r) * FEW_UP;
-                const bool shared = g == 0;
-                const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(s_exp[g]), n = __builtin_amdgcn_readfirstlane(s_n[g]);
-                const int slot = s_slot[g][r16 < n ? r16 : 0];         // lanes past the rows repeat the first
-                const uint32_t tok = shared ? slot : slot / k;
-                const int64_t ldw = (int64_t)d * 128 / LK;
-                const int64_t row0 = (shared ? 0 : (int64_t)e * a.inter) + f0;     // the item's first weight row
-                const uint8_t* s = nullptr;
-                if constexpr (ST == ST_MX4)
-                    s = (shared ? (r16 < 8 ? a.S1s : a.S3s) : (r16 < 8 ? a.W1s : a.W3s)) + (row0 + (r16 & 7)) * (d / 32);
-                if constexpr (ST == ST_FP8)            // the lane's results are of features 4 q .. 4 q + 3
-                    s = (shared ? (q < 2 ? a.S1s : a.S3s) : (q < 2 ? a.W1s : a.W3s)) + row0 / 128 * (d / 128) * 4;
-                const WRows wr = weight_rows<ST>((shared ? a.S1 : a.W1) + row0 * ldw, (shared ? a.S3 : a.W3) + row0 * ldw, s, ldw, d, lane);
-                const ARows ax = {X_LDS ? act : a.x, X_LDS ? act_s : a.xs, tok * xstr + 16 * q, tok * xsstr, wr.half};
-                const int nu = stream_units_of<ST>(d);
-                f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-                Stream<ST, X_LDS, DU> st;
-                st.begin(wr, ax, nu);
-                st.run(acc, ax, 0, nu, nu, tiles[wave], lane);
-                // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
-                float hv[4];
-#pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
-                    if constexpr (BF) {
-                        round_bf16x2(gg, uu);
-                        hv[r] = silu_mul_fast(gg, uu);
-                    } else {
-                        hv[r] = silu_mul(gg, uu);
-                    }
-                }
-                if (q < 2 && r16 < n) {
-                    const int64_t hrow = shared ? slots + slot : slot;
-                    put4<BF>(a.h + (hrow * a.inter_max + f0 + 4 * q) * AB, hv);
-                }
-                asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-                if (lane == 0) bump(&a.up_done[g * FEW_PAD]);
+    // ---- jobs.  Numbers of items [0, n_up): FEW_NW wavefronts' up jobs each; then ng * ncol down items.
+    const int ng = 1 + n_sel, nu_s = args.inter_s / FEW_UP, nu_r = args.inter / FEW_UP, ncol = d / FEW_DN;
+    const int n_wup = nu_s + n_sel * nu_r, n_up = (n_wup + FEW_NW - 1) / FEW_NW, total = n_up + ng * ncol;
+    int round = 0;                                     // of item numbers
+    // The block's item of this round: its first lane leaves it in LDS, the other wavefronts find it there.  In the up
+    // jobs wavefronts pass from round to round without waiting for each other; the barrier every 32 rounds (below)
+    // keeps the fastest from overwriting a number that the slowest has not read.
+    auto job_of_round = [&]() -> FewJob {
+        uint64_t got;
+        while ((int)((got = s_ticket[round % 64]) >> 32) != round + 1) __builtin_amdgcn_s_sleep(1);
+        const int item = __builtin_amdgcn_readfirstlane((int)got);
+        if (item >= total) return {FEW_NONE, 0, 0};    // every block comes to a number past the end
+        if (item >= n_up) return {FEW_DN_JOB, (item - n_up) / ncol, (item - n_up) % ncol};
+        const int it = item * FEW_NW + wave;
+        if (it >= n_wup) return {FEW_IDLE, 0, 0};
+        if (it < nu_s) return {FEW_UP_JOB, 0, it * FEW_UP};
+        return {FEW_UP_JOB, 1 + (it - nu_s) / nu_r, (it - nu_s) % nu_r * FEW_UP};
+    };
+    Stream<ST, X_LDS, D> st;
+    // The arguments are read anew for each job: kept over the loop they would take most scalar registers.
+    auto arguments = [&]() -> KernArgs {
+        KernArgs p = (KernArgs)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(p));
+        return p;
+    };
+    auto up_rows = [&](const FewJob& job, int& tok, int& slot, int& n) {
+        n = __builtin_amdgcn_readfirstlane(s_n[job.g]);
+        slot = s_slot[job.g][r16 < n ? r16 : 0];       // lanes past the rows repeat the first
+        tok = job.g ? slot / k : slot;
+    };
+    // The stream goes on with this job's weights.
+    auto start = [&](const FewJob& job) {
+        const auto& a = *arguments();
+        if (job.kind == FEW_UP_JOB) {                  // eight rows of W1 and the same eight of W3
+            const int64_t ldw = (int64_t)d * 128 / LK;
+            const int e = job.g ? __builtin_amdgcn_readfirstlane(s_exp[job.g]) : 0;
+            const int64_t row0 = (int64_t)e * a.inter + job.at;
+            const uint8_t* s = nullptr;
+            if constexpr (ST == ST_MX4)
+                s = (job.g ? (r16 < 8 ? a.W1s : a.W3s) : (r16 < 8 ? a.S1s : a.S3s)) + (row0 + (r16 & 7)) * (d / 32);
+            if constexpr (ST == ST_FP8)                // the lane's results are of features 4 q .. 4 q + 3
+                s = (job.g ? (q < 2 ? a.W1s : a.W3s) : (q < 2 ? a.S1s : a.S3s)) + row0 / 128 * (d / 128) * 4;
+            st.start(weight_rows<ST>((job.g ? a.W1 : a.S1) + row0 * ldw, (job.g ? a.W3 : a.S3) + row0 * ldw, s, ldw, d, lane),
+                     stream_units_of<ST>(d));
+            if constexpr (!X_LDS) {
+                int tok, slot, n;
+                up_rows(job, tok, slot, n);
+                st.ar = {a.x, a.xs, (uint32_t)tok * xstr + 16 * q, (uint32_t)tok * xsstr, st.wr.half};
             }
-            __syncthreads();
-            continue;
+        } else if (job.kind == FEW_DN_JOB) {           // 16 rows of W2
+            const int K = job.g ? a.inter : a.inter_s;
+            const int64_t ldw = (int64_t)K * 128 / LK;
+            const int e = job.g ? __builtin_amdgcn_readfirstlane(s_exp[job.g]) : 0;
+            const int64_t row0 = (int64_t)e * d + job.at * FEW_DN + wave * 16;
+            const uint8_t* s = nullptr;
+            if constexpr (ST == ST_MX4) s = (job.g ? a.W2s : a.S2s) + (row0 + r16) * (K / 32);
+            if constexpr (ST == ST_FP8) s = (job.g ? a.W2s : a.S2s) + row0 / 128 * (K / 128) * 4;
+            const uint8_t* p0 = (job.g ? a.W2 : a.S2) + row0 * ldw;
+            st.start(weight_rows<ST>(p0, p0 + 8 * ldw, s, ldw, K, lane), stream_units_of<ST>(K));
+            if constexpr (!X_LDS) st.ar = {a.x, a.xs, (uint32_t)(16 * q), 0, 0};       // travels along unused
+        } else {
+            st.nu = 1;                                 // nothing follows: the last unit again, unused
         }
-
-        // ---- 16 output features of one expert a wavefront, over the whole K
-        const int v = item - n_up, g = v / ncol, c = v % ncol;
-        const bool shared = g == 0;
-        const int e = shared ? 0 : __builtin_amdgcn_readfirstlane(s_exp[g]), n = __builtin_amdgcn_readfirstlane(s_n[g]), K = shared ? a.inter_s : a.inter;
-        const int64_t ldw = (int64_t)K * 128 / LK;
-        const int64_t row0 = (shared ? 0 : (int64_t)e * d) + c * FEW_DN + wave * 16;   // the wavefront's first row
-        const uint8_t* s = nullptr;
-        if constexpr (ST == ST_MX4) s = (shared ? a.S2s : a.W2s) + (row0 + r16) * (K / 32);
-        if constexpr (ST == ST_FP8) s = (shared ? a.S2s : a.W2s) + row0 / 128 * (K / 128) * 4;
-        const uint8_t* p0 = (shared ? a.S2 : a.W2) + row0 * ldw;
-        const WRows wr = weight_rows<ST>(p0, p0 + 8 * ldw, s, ldw, K, lane);
-        const int nu = stream_units_of<ST>(K);
-        Stream<ST, true, DD> st;
-        st.begin(wr, {}, nu);                          // these need no h
-        if (tid == 0) {
-            const int need = shared ? nu_s : nu_r;
-            while (__hip_atomic_load(&a.up_done[g * FEW_PAD], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
-                __builtin_amdgcn_s_sleep(8);
-        }
-        __syncthreads();
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-        const int ar = r16 < n ? r16 : 0;
-        for (int k0 = 0; k0 < K; k0 += KC) {
-            const int kc = min(KC, K - k0);            // elements of this chunk
-            if (k0) __syncthreads();                   // the chunk before is used up
-            const int vecs = kc / 8;                   // 8 elements a thread; a multiple of 16
-            for (int i = tid; i < n * vecs; i += NT) {
-                const int r = i / vecs, p = i - r * vecs, sl = s_slot[g][r];
-                const uint8_t* src = a.h + ((int64_t)(shared ? slots + sl : sl) * a.inter_max + k0 + p * 8) * AB;
-                uint8_t* dst = act + r * HSTR;
-                if constexpr (ST == ST_F32) {
-                    *(uint4*)(dst + p * 32) = get128(src);
-                    *(uint4*)(dst + p * 32 + 16) = get128(src + 16);
-                } else {
-                    const uint4 raw = get128(src);
-                    if constexpr (ST == ST_BF16) {
-                        *(uint4*)(dst + p * 16) = raw;
-                    } else {
-                        float hv[8];
-                        bf16x8_to_f32(raw, hv);
-                        if constexpr (ST == ST_MX4) {
-                            const uint32_t sc = mx_scale_code<false>(quad_max(mx_amax8(hv)));
-                            *(uint2*)(dst + p * 8) = sc == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(hv, sc);
-                            if ((p & 3) == 0) act_s[r * (KC / 32) + p / 4] = (uint8_t)sc;
-                        } else {
-                            float sc;
-                            *(uint2*)(dst + p * 8) = quant8_e4m3(hv, sc);
-                            if ((p & 15) == 0) ((float*)act_s)[r * (KC / 128) + p / 16] = sc;
-                        }
-                    }
-                }
-            }
-            __syncthreads();
-            const ARows hrow = {act, act_s, (uint32_t)(ar * HSTR + 16 * q),
-                                (uint32_t)(ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4)), ST == ST_MX4 && kc % 256 ? kc / 256 : -1};
-            st.run(acc, hrow, k0 / LK, k0 / LK + stream_units_of<ST>(kc), nu, tiles[wave], lane);
-        }
-        // this lane: features 4 q .. 4 q + 3 of the group's row r16
-        if (r16 < n) {
-            const int sl = s_slot[g][r16];
-            const float o[4] = {acc[0], acc[1], acc[2], acc[3]};
-            put4<BF>(a.y_rows + ((int64_t)(shared ? slots + sl : sl) * d + c * FEW_DN + wave * 16 + 4 * q) * AB, o);
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
-        if (tid == 0) s_last = bump(&a.col_done[c * FEW_PAD]) == ng - 1;
-        __syncthreads();
+        if constexpr (!X_LDS) st.ar_step = job.kind == FEW_UP_JOB;
+    };
+    auto next_job = [&]() -> FewJob {
+        round++;
+        if (tid == 0) s_ticket[round % 64] = (uint64_t)(round + 1) << 32 | (uint32_t)ticket;
+        return job_of_round();
+    };
+    // Up items whose h is stored but not yet counted (group, or -1): vector memory operations complete in order, so
+    // once a later load has been used the stores are done; before a wait for others they are waited for.
+    int stored = -1;
+    auto count_stored = [&](bool drain) {
+        if (stored < 0) return;
+        if (drain) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if (lane == 0) bump(&arguments()->up_done[stored * FEW_PAD]);
+        stored = -1;
+    };
+    // The down item whose column count is on its way (column range, or -1).
+    int counted = -1, count = 0;
+    // Sums the experts' outputs of that item's columns if it was their last: by ascending expert, then the shared one.
+    // Every wavefront comes here; behind a barrier.
+    auto combine_if_last = [&] {
+        if (counted < 0) return;
         if (s_last) {
-            // the experts' outputs for these columns are there: the combine, by ascending expert, then the shared one
+            const auto& a = *arguments();
             constexpr int VE = 16 / AB;                // elements of a vector
             constexpr int VR = FEW_DN / VE;            // vectors of a row
             for (int i = tid; i < T * VR; i += NT) {
                 const int t = i / VR;
-                const int64_t col = c * FEW_DN + i % VR * VE;
+                const int64_t col = counted * FEW_DN + i % VR * VE;
                 float sum[VE];
 #pragma unroll
                 for (int j = 0; j < VE; j++) sum[j] = 0.f;
@@ -454,6 +410,125 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs a)
                 *(uint4*)(a.y + ((int64_t)t * d + col) * AB) = o;
             }
         }
+        counted = -1;
+    };
+
+    FewJob job = job_of_round();
+    bool filled = false;                               // the job's first units are on their way
+    while (job.kind != FEW_NONE) {
+        if (round % 32 == 31) __syncthreads();
+        if (!filled && job.kind != FEW_IDLE) {
+            start(job);
+            st.fill(lane);
+        }
+        if (tid == 0) ticket = bump(arguments()->ticket);
+        FewJob then;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        if (job.kind == FEW_IDLE) {
+            then = next_job();
+            filled = false;
+        } else if (job.kind == FEW_UP_JOB) {
+            int tok, slot, n;
+            up_rows(job, tok, slot, n);
+            const int nu = stream_units_of<ST>(d);
+            const ARows ax = {act, act_s, (uint32_t)tok * xstr + 16 * q, (uint32_t)tok * xsstr, st.wr.half};
+            int u = 0;
+            for (; u + D < nu; u += D) st.template round<true>(acc, ax, u, nu, 0, tiles[wave], lane);
+            then = next_job();
+            start(then);
+            st.template round<true>(acc, ax, u, nu, 0, tiles[wave], lane);
+            filled = then.kind != FEW_IDLE;
+            count_stored(nu <= D);
+            // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
+            float hv[4];
+#pragma unroll
+            for (int r = 0; r < 4; r++) {
+                float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
+                if constexpr (BF) {
+                    round_bf16x2(gg, uu);
+                    hv[r] = silu_mul_fast(gg, uu);
+                } else {
+                    hv[r] = silu_mul(gg, uu);
+                }
+            }
+            const auto& a = *arguments();
+            if (q < 2 && r16 < n) put4<BF>(a.h + ((int64_t)(job.g ? slot : slots + slot) * a.inter_max + job.at + 4 * q) * AB, hv);
+            stored = job.g;
+        } else {
+            const auto& a = *arguments();
+            const int n = __builtin_amdgcn_readfirstlane(s_n[job.g]), K = job.g ? a.inter : a.inter_s, nu = stream_units_of<ST>(K);
+            count_stored(true);                        // before the wait: it may be for these
+            if (tid == 0) {
+                const int need = job.g ? nu_r : nu_s;
+                while (__hip_atomic_load(&a.up_done[job.g * FEW_PAD], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
+                    __builtin_amdgcn_s_sleep(4);
+                s_last = count == ng - 1;
+            }
+            __syncthreads();                           // also: every wavefront is past the up jobs, x is not needed any more
+            combine_if_last();
+            const int ar = r16 < n ? r16 : 0;
+            for (int k0 = 0;; k0 += KC) {
+                // elements [k0, k0 + kc) of the group's rows of h into LDS, as the linear takes them
+                const int kc = min(KC, K - k0), vecs = kc / 8;         // 8 elements a thread; a multiple of 16
+                if (k0) __syncthreads();               // the chunk before is used up
+                for (int i = tid; i < n * vecs; i += NT) {
+                    const int r = i / vecs, p = i - r * vecs, sl = s_slot[job.g][r];
+                    const uint8_t* src = a.h + ((int64_t)(job.g ? sl : slots + sl) * a.inter_max + k0 + p * 8) * AB;
+                    uint8_t* dst = act + r * HSTR;
+                    if constexpr (ST == ST_F32) {
+                        *(uint4*)(dst + p * 32) = get128(src);
+                        *(uint4*)(dst + p * 32 + 16) = get128(src + 16);
+                    } else {
+                        const uint4 raw = get128(src);
+                        if constexpr (ST == ST_BF16) {
+                            *(uint4*)(dst + p * 16) = raw;
+                        } else {
+                            float hv[8];
+                            bf16x8_to_f32(raw, hv);
+                            if constexpr (ST == ST_MX4) {
+                                const uint32_t sc = mx_scale_code<false>(quad_max(mx_amax8(hv)));
+                                *(uint2*)(dst + p * 8) = sc == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(hv, sc);
+                                if ((p & 3) == 0) act_s[r * (KC / 32) + p / 4] = (uint8_t)sc;
+                            } else {
+                                float sc;
+                                *(uint2*)(dst + p * 8) = quant8_e4m3(hv, sc);
+                                if ((p & 15) == 0) ((float*)act_s)[r * (KC / 128) + p / 16] = sc;
+                            }
+                        }
+                    }
+                }
+                __syncthreads();
+                const ARows hrow = {act, act_s, (uint32_t)(ar * HSTR + 16 * q),
+                                    (uint32_t)(ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4)), ST == ST_MX4 && kc % 256 ? kc / 256 : -1};
+                const int u0 = k0 / LK, u1 = u0 + stream_units_of<ST>(kc);
+                int u = u0;
+                for (; u < u1 && u + D < nu; u += D) st.template round<true, true>(acc, hrow, u, u1, u0, tiles[wave], lane);
+                if (u < u1) {                          // the matrix's last round
+                    then = next_job();
+                    start(then);
+                    st.template round<true, true>(acc, hrow, u, u1, u0, tiles[wave], lane);
+                    break;
+                }
+            }
+            filled = then.kind != FEW_IDLE;
+            // this lane: features 4 q .. 4 q + 3 of the group's row r16
+            if (r16 < n) {
+                const int sl = s_slot[job.g][r16];
+                const float o[4] = {acc[0], acc[1], acc[2], acc[3]};
+                put4<BF>(a.y_rows + ((int64_t)(job.g ? sl : slots + sl) * d + job.at * FEW_DN + wave * 16 + 4 * q) * AB, o);
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            __syncthreads();
+            if (tid == 0) count = bump(&a.col_done[job.at * FEW_PAD]);
+            counted = job.at;
+        }
+        job = then;
+    }
+    count_stored(true);
+    if (counted >= 0) {
+        if (tid == 0) s_last = count == ng - 1;
+        __syncthreads();
+        combine_if_last();
     }
 }
 
@@ -516,7 +591,7 @@ static hipError_t launch_few_t(const moe_shape_t& s, const void* x, const float*
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     // a block for each of the card's 256 CUs (any number is right: see above)
-    const int64_t row = s.d * FewAct<ST>::bytes + 16;
+    const int64_t row = s.d * FewAct<ST>::bytes + 16;  // of x in LDS
     if (s.T * row <= FEW_XBYTES && s.T * s.d / 32 <= FEW_XSCALES) few_layer_kernel<ST, true><<<256, 64 * FEW_NW, 0, stream>>>(a);
     else few_layer_kernel<ST, false><<<256, 64 * FEW_NW, 0, stream>>>(a);
     return hipGetLastError();

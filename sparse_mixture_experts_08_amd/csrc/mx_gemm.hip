@@ -84,11 +84,17 @@ __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
             const int64_t arow = UP ? g.row_token[row0 + r] : row0 + r;
             *(uint32_t*)(xs + r * (XK / 32) + p * 4) = *(const uint32_t*)(bytes(g.As) + arow * g.ldas + k0 / 32 + p * 4);
         }
-        if (k0 == 0) st.begin(wr, {}, nu);             // behind the activations' loads, so that these do not wait for it
+        if (k0 == 0) {                                 // behind the activations' loads, so that these do not wait for it
+            st.start(wr, nu);
+            st.fill(lane);
+        }
         lds_barrier();
         const int ar = r16 < rows ? r16 : 0;           // lanes past the tile's rows repeat its first row (never stored)
         const ARows a = {xb, xs, (uint32_t)(ar * XSTR + 16 * q), (uint32_t)(ar * (XK / 32)), kc % 256 ? kc / 256 : -1};
-        st.run(acc, a, k0 / 256, k0 / 256 + stream_units_of<ST_MX4>(kc), nu, tiles[wave], lane);
+        const int u0 = k0 / 256, u1 = u0 + stream_units_of<ST_MX4>(kc);
+        int u = u0;
+        for (; u < u1 && u + D < nu; u += D) st.template round<true>(acc, a, u, u1, u0, tiles[wave], lane);
+        if (u < u1) st.template round<false>(acc, a, u, u1, u0, tiles[wave], lane);
     }
     __syncthreads();
 

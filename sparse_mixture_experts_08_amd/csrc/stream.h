@@ -50,37 +50,33 @@ struct WRows {
     int half;                                          // MXFP4: the unit that is only half there, or -1
     uint32_t offh;                                     // ... and the offset for it: chunks 4 .. 7 read 0 .. 3 again
     const uint8_t* s;                                  // MXFP4: scale bytes of row l % 16; fp8: its block row's floats
+    int ns;                                            // 4-byte words there
 };
+
+// A pointer that is the same in every lane, as a scalar.
+__device__ __forceinline__ const uint8_t* uniform(const uint8_t* p)
+{
+    const uint64_t v = (uint64_t)p;
+    return (const uint8_t*)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                            (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
 
 // ld: bytes between rows; K: the rows' length.
 template <int ST>
 __device__ __forceinline__ WRows weight_rows(const uint8_t* p0, const uint8_t* p1, const uint8_t* s, int64_t ld, int K, int lane)
 {
     const uint32_t row = (lane >> 3) * (uint32_t)ld;
-    return {p0, p1, row + (lane & 7) * 16, ST == ST_MX4 && K % 256 ? K / 256 : -1, row + (lane & 3) * 16, s};
+    return {uniform(p0), uniform(p1), row + (lane & 7) * 16, ST == ST_MX4 && K % 256 ? K / 256 : -1, row + (lane & 3) * 16, s, K / 128};
 }
 
-// The lane's part of one unit of weights on its way, with its scales.
+// The lane's part of one unit of weights on its way.
 template <int ST> struct WUnit {
     i32x4 p[2];                                        // rows l / 8 and 8 + l / 8
-    uint32_t s[ST == ST_MX4 ? 2 : 1];                  // MXFP4: row l % 16's scale bytes, 128 elements each; fp8: scale bits
-    // The next unit of r, and r moved on by n units (0 or 1); h: the unit is only half there.
-    __device__ __forceinline__ void load(WRows& r, bool h, int n)
+    __device__ __forceinline__ void load(const WRows& r, int u)
     {
-        const uint32_t o = ST == ST_MX4 && h ? r.offh : r.off;
-        p[0] = __builtin_nontemporal_load((const i32x4*)(r.p0 + o));
-        p[1] = __builtin_nontemporal_load((const i32x4*)(r.p1 + o));
-        r.p0 += 128 * n;
-        r.p1 += 128 * n;
-        if constexpr (ST == ST_FP8) {
-            s[0] = *(const uint32_t*)r.s;
-            r.s += 4 * n;
-        }
-        if constexpr (ST == ST_MX4) {
-            s[0] = ((const uint32_t*)r.s)[0];
-            s[1] = ((const uint32_t*)r.s)[h ? 0 : 1];
-            r.s += 8 * n;
-        }
+        const uint32_t o = ST == ST_MX4 && u == r.half ? r.offh : r.off;
+        p[0] = __builtin_nontemporal_load((const i32x4*)(r.p0 + (int64_t)u * 128 + o));
+        p[1] = __builtin_nontemporal_load((const i32x4*)(r.p1 + (int64_t)u * 128 + o));
     }
     // Into the wavefront's tile: chunk c of row r at chunk c ^ f(r), f(r) = (r ^ (r >> 3 & 1)) & 7, so that the 16
     // rows of a read fall on distinct banks.
@@ -120,13 +116,14 @@ template <int ST> struct AUnit {
             const uint8_t* c = r.s + (int64_t)u * 8;
             s[0] = *(const uint32_t*)(c + r.soff);
             s[1] = *(const uint32_t*)(c + (h ? 0 : 4) + r.soff);
+            if (h) p[2] = p[3] = (i32x4){0, 0, 0, 0};  // the half that is not there
         }
     }
 };
 
-// acc += W unit . A unit, w the operand pieces, ws the scales; whole: both halves of an MXFP4 unit; q = lane / 16.
+// acc += W unit . A unit, w the operand pieces, ws the scales (MXFP4: one word a half); q = lane / 16.
 template <int ST>
-__device__ __forceinline__ void stream_mma(f32x4& acc, const i32x4 (&w)[2], const uint32_t* ws, const AUnit<ST>& a, bool whole, int q)
+__device__ __forceinline__ void stream_mma(f32x4& acc, const i32x4 (&w)[2], const uint32_t (&ws)[2], const AUnit<ST>& a, int q)
 {
     if constexpr (ST == ST_F32) {
 #pragma unroll
@@ -151,7 +148,6 @@ __device__ __forceinline__ void stream_mma(f32x4& acc, const i32x4 (&w)[2], cons
     } else {
 #pragma unroll
         for (int j = 0; j < 2; j++) {
-            if (j == 1 && !whole) break;
             const i32x8 wv = {w[j].x, w[j].y, w[j].z, w[j].w, 0, 0, 0, 0};
             const i32x4 lo = a.p[2 * j], hi = a.p[2 * j + 1];
             const i32x8 av = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
@@ -161,75 +157,83 @@ __device__ __forceinline__ void stream_mma(f32x4& acc, const i32x4 (&w)[2], cons
     }
 }
 
-// acc += W . A with D weight units in flight.  tile: the wavefront's own LDS.  A_LDS: the activations lie in LDS and
-// are read as they are needed; otherwise their units travel with the weights'.  (Vector loads come back in order, so
-// the wait for an activation load that was issued later than far-ahead weight loads would be a wait for those.)
-// The scheduling barriers keep the loads in the order of their
-// units, in the prologue as in the loop: a unit's wait then leaves the D - 1 units behind it in flight.  (Without
-// them the compiler orders the prologue its own way, and the loop's waits, which have to hold for both, drain almost
-// every load.)
+// A stream of weight units through registers, D in flight, one matrix after the other.  fill() issues the first D
+// units; a round multiplies D units and, with MORE, issues the D after them in their places: a matrix's rounds are
+// all alike, and before its last one start() may name the matrix that follows, so that the loads never pause.  Past
+// a matrix's end its last unit is loaded again (nu need not be a multiple of D); nothing is multiplied there.
+// tile: the wavefront's own LDS.  A_LDS: the activations lie in LDS and are read as they are needed; otherwise their
+// units travel with the weights'.  (Vector loads come back in order, so the wait for an activation load that was
+// issued later than far-ahead weight loads would be a wait for those.)  Scales: one word load a lane brings the words
+// of several units (MXFP4: two units, the word 2 u + q of row l % 16 to lane l; fp8: four units, the word u + l % 4 of
+// the lane's block row), handed around by lane permutes; as a load per unit and half they would be as many line
+// requests as the weights.  The scheduling barriers keep the loads in the order of their units, with no branch around
+// them: a unit's wait then leaves the D - 1 units behind it in flight.  (Left alone, the compiler orders the first
+// loads its own way, and the waits, which have to hold for them too, drain almost every load.)
 template <int ST, bool A_LDS, int D> struct Stream {
+    static constexpr int SU = ST == ST_MX4 ? 2 : ST == ST_FP8 ? 4 : 1;         // units a scale load serves
+    static_assert(D % SU == 0, "whole scale loads a round");
     WUnit<ST> w[D];
+    uint32_t s[D / SU];
     AUnit<ST> a[A_LDS ? 1 : D];
-    WRows wr;                                          // from the next unit to load on
-    int next;
+    WRows wr;
+    ARows ar;                                          // !A_LDS: the activations that travel along, and whether they
+    int ar_step = 1;                                   // advance (0: the first unit again and again, unused)
+    int next, nu;                                      // the unit to load next; the matrix's units
 
-    __device__ __forceinline__ void load(int j, const ARows& ar, int n = 1)
-    {
-        w[j].load(wr, next == wr.half, n);
-        if constexpr (!A_LDS) a[j].load(ar, next);
-        next += n;
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    // The first units of nu; of fewer than D, the last one again.
-    __device__ __forceinline__ void begin(const WRows& r, const ARows& ar, int nu)
+    __device__ __forceinline__ void start(const WRows& r, int units)
     {
         wr = r;
         next = 0;
-#pragma unroll
-        for (int j = 0; j < D; j++)
-            load(j, ar, j + 1 < nu || j == D - 1);
+        nu = units;
     }
-    __device__ __forceinline__ void mma(int j, f32x4& acc, const ARows& ar, int u, int ua, uint8_t* tile, int lane)
+    __device__ __forceinline__ void load(int j, int lane)
     {
-        i32x4 f[2];
-        w[j].put(tile, lane);
-        if constexpr (A_LDS) {
-            AUnit<ST> al;
-            al.load(ar, ua);
-            WUnit<ST>::get(tile, lane, f);
-            stream_mma<ST>(acc, f, w[j].s, al, u != wr.half, lane >> 4);
-        } else {
-            WUnit<ST>::get(tile, lane, f);
-            stream_mma<ST>(acc, f, w[j].s, a[j], u != wr.half, lane >> 4);
+        const int u = min(next, nu - 1);
+        w[j].load(wr, u);
+        if constexpr (ST == ST_MX4 || ST == ST_FP8) {
+            if (j % SU == SU - 1) {                    // behind the last of the units it serves: the old words are used up
+                const int first = next - (SU - 1), i = ST == ST_MX4 ? 2 * first + (lane >> 4) : first + (lane & 3);
+                s[j / SU] = ((const uint32_t*)wr.s)[min(i, wr.ns - 1)];
+            }
         }
+        if constexpr (!A_LDS) a[j].load(ar, u * ar_step);
+        next++;
         __builtin_amdgcn_sched_barrier(0);
     }
-    // Units [u0, u1) of nu, u0 a multiple of D; in LDS ar counts its units from u0.  The rounds whose every unit has
-    // a successor to load run in a loop without a branch; the last two rounds stand by themselves, so that nothing
-    // past the end is loaded.
-    __device__ __forceinline__ void run(f32x4& acc, const ARows& ar, int u0, int u1, int nu, uint8_t* tile, int lane)
+    __device__ __forceinline__ void fill(int lane)
     {
-        int u = u0;
-        for (; u < u1 && u + 2 * D <= nu; u += D) {
 #pragma unroll
-            for (int j = 0; j < D; j++) {
-                mma(j, acc, ar, u + j, u + j - u0, tile, lane);
-                load(j, ar);
+        for (int j = 0; j < D; j++) load(j, lane);
+    }
+    // acc += units u .. u + D - 1, of those below u1.  al: activations, if they lie in LDS (LDS: in any case), their
+    // units counted from ua.
+    template <bool MORE, bool LDS = A_LDS>
+    __device__ __forceinline__ void round(f32x4& acc, const ARows& al, int u, int u1, int ua, uint8_t* tile, int lane)
+    {
+#pragma unroll
+        for (int j = 0; j < D; j++) {
+            if (u + j < u1) {
+                i32x4 f[2];
+                uint32_t ws[2] = {0, 0};
+                w[j].put(tile, lane);
+                if constexpr (ST == ST_MX4) {          // words 2 j, 2 j + 1 of the four that the row's lanes hold
+                    ws[0] = __shfl(s[j / 2], (lane & 15) + 32 * (j % 2), 64);
+                    ws[1] = __shfl(s[j / 2], (lane & 15) + 32 * (j % 2) + 16, 64);
+                } else if constexpr (ST == ST_FP8) {
+                    ws[0] = __shfl(s[j / 4], (lane & 60) + j % 4, 64);
+                }
+                if constexpr (LDS) {
+                    AUnit<ST> x;
+                    x.load(al, u + j - ua);
+                    WUnit<ST>::get(tile, lane, f);
+                    stream_mma<ST>(acc, f, ws, x, lane >> 4);
+                } else {
+                    WUnit<ST>::get(tile, lane, f);
+                    stream_mma<ST>(acc, f, ws, a[j], lane >> 4);
+                }
             }
-        }
-        if (u < u1 && u + D <= nu) {
-#pragma unroll
-            for (int j = 0; j < D; j++) {
-                mma(j, acc, ar, u + j, u + j - u0, tile, lane);
-                if (u + j + D < nu) load(j, ar);
-            }
-            u += D;
-        }
-        if (u < u1) {
-#pragma unroll
-            for (int j = 0; j < D; j++)
-                if (u + j < u1) mma(j, acc, ar, u + j, u + j - u0, tile, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (MORE) load(j, lane);
         }
     }
 };

@@ -28,12 +28,23 @@ __device__ __forceinline__ uint64_t logit_key(float l, int e)
 
 __device__ __forceinline__ int key_expert(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
-// Maximum of a 64-bit value over groups of W consecutive lanes.
+// Maximum of a 64-bit value over groups of W consecutive lanes.  Within 16 lanes (a DPP row) by DPP moves, a few
+// cycles each, instead of LDS permutes; every lane of a row must be active.
+template <int CTRL> __device__ __forceinline__ uint64_t dpp_max_u64(uint64_t v)
+{
+    const uint64_t o = ((uint64_t)dpp_u32<CTRL>((uint32_t)(v >> 32)) << 32) | dpp_u32<CTRL>((uint32_t)v);
+    return o > v ? o : v;
+}
 template <int W>
 __device__ __forceinline__ uint64_t group_max_u64(uint64_t v)
 {
+    static_assert(W >= 16, "whole DPP rows");
+    v = dpp_max_u64<0xB1>(v);                          // quad_perm [1, 0, 3, 2]
+    v = dpp_max_u64<0x4E>(v);                          // quad_perm [2, 3, 0, 1]
+    v = dpp_max_u64<0x141>(v);                         // row_half_mirror
+    v = dpp_max_u64<0x140>(v);                         // row_mirror
 #pragma unroll
-    for (int off = W / 2; off >= 1; off >>= 1) {
+    for (int off = W / 2; off >= 16; off >>= 1) {
         const uint32_t lo = __shfl_xor((uint32_t)v, off, W), hi = __shfl_xor((uint32_t)(v >> 32), off, W);
         const uint64_t o = ((uint64_t)hi << 32) | lo;
         v = o > v ? o : v;
