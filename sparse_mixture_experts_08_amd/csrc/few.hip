@@ -60,36 +60,45 @@ struct FewArgs {
 // ---------------------------------------------------------------------------------------------------
 constexpr int FEW_NT1 = 1024;                          // threads per block of launch 1
 
-template <typename XT> __device__ __forceinline__ void load4(const XT* p, double (&v)[4]);
-template <> __device__ __forceinline__ void load4<uint16_t>(const uint16_t* p, double (&v)[4])
-{
-    const uint2 r = *(const uint2*)p;
-    v[0] = (double)__uint_as_float(r.x << 16);
-    v[1] = (double)__uint_as_float(r.x & 0xFFFF0000u);
-    v[2] = (double)__uint_as_float(r.y << 16);
-    v[3] = (double)__uint_as_float(r.y & 0xFFFF0000u);
-}
-template <> __device__ __forceinline__ void load4<float>(const float* p, double (&v)[4])
-{
-    const float4 r = *(const float4*)p;
-    v[0] = (double)r.x; v[1] = (double)r.y; v[2] = (double)r.z; v[3] = (double)r.w;
-}
+// Eight consecutive elements, raw from the load to their use.
+template <typename XT> struct Few8;
+template <> struct Few8<uint16_t> {
+    uint4 r;
+    __device__ __forceinline__ void load(const uint16_t* p) { r = *(const uint4*)p; }
+    __device__ __forceinline__ void get(float (&v)[8]) const { bf16x8_to_f32(r, v); }
+};
+template <> struct Few8<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p)
+    {
+        a = ((const float4*)p)[0];
+        b = ((const float4*)p)[1];
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const
+    {
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    }
+};
 
 // Sums of TM values over a wavefront, value t to the lanes whose top log2(TM) bits are t (bit 5 first): each step
 // halves the values that a lane keeps and adds the partner's, so TM values take TM - 1 exchanges and then one per
 // remaining bit, against 6 TM.
-template <int TM> __device__ __forceinline__ double wave_sums(double (&v)[TM], int lane)
+template <int N, int TM> __device__ __forceinline__ void wave_sums_step(double (&v)[TM], int lane, int off)
 {
-    int off = 32;
-#pragma unroll
-    for (int n = TM / 2; n >= 1; n >>= 1, off >>= 1) {
+    if constexpr (N >= 1) {
         const bool hi = lane & off;
 #pragma unroll
-        for (int i = 0; i < n; i++) {
-            const double other = __shfl_xor(hi ? v[i] : v[n + i], off, 64);
-            v[i] = (hi ? v[n + i] : v[i]) + other;
+        for (int i = 0; i < N; i++) {
+            const double keep = hi ? v[N + i] : v[i], give = hi ? v[i] : v[N + i];
+            v[i] = keep + __shfl_xor(give, off, 64);
         }
+        wave_sums_step<N / 2, TM>(v, lane, off / 2);
     }
+}
+template <int TM> __device__ __forceinline__ double wave_sums(double (&v)[TM], int lane)
+{
+    wave_sums_step<TM / 2, TM>(v, lane, 32);
 #pragma unroll
     for (int o = 32 / TM; o >= 1; o >>= 1) v[0] += __shfl_xor(v[0], o, 64);
     return v[0];
@@ -111,15 +120,25 @@ __global__ __launch_bounds__(FEW_NT1) void few_prepare_kernel(const void* __rest
 #pragma unroll
         for (int t = 0; t < TM; t++) acc[t] = 0.0;
         const float* wrow = Wg + (size_t)b * d;
-        for (int i = tid * 4; i < d; i += 4 * FEW_NT1) {
-            double w[4];
-            load4<float>(wrow + i, w);
+        for (int i = tid * 8; i < d; i += 8 * FEW_NT1) {
+            constexpr int TC = ST == ST_F32 && TM > 8 ? 8 : TM;        // tokens at a time: their loads first, in flight together
+            Few8<float> wr;
+            wr.load(wrow + i);
 #pragma unroll
-            for (int t = 0; t < TM; t++) {
-                double v[4];
-                load4<XT>(x + (size_t)min(t, T - 1) * d + i, v);
+            for (int t0 = 0; t0 < TM; t0 += TC) {
+                Few8<XT> xr[TC];
 #pragma unroll
-                for (int e = 0; e < 4; e++) acc[t] = __builtin_fma(v[e], w[e], acc[t]);
+                for (int t = 0; t < TC; t++) xr[t].load(x + (size_t)min(t0 + t, T - 1) * d + i);
+                __builtin_amdgcn_sched_barrier(0);
+                float w[8];
+                wr.get(w);
+#pragma unroll
+                for (int t = 0; t < TC; t++) {
+                    float v[8];
+                    xr[t].get(v);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) acc[t0 + t] = __builtin_fma((double)v[e], (double)w[e], acc[t0 + t]);
+                }
             }
         }
         const int lane = tid & 63;
@@ -200,11 +219,15 @@ template <> struct FewAct<ST_MX4> { static constexpr int bytes = 1; };
 // X_LDS: x fits (rows of d elements) and is kept there for the up items.
 constexpr int FEW_ROW = 7168, FEW_XBYTES = 16 * (FEW_ROW + 16), FEW_XSCALES = 16 * FEW_ROW / 32;
 
+// First unit of wavefront w's part of nu units, at a multiple of four (a scale load's units).
+__device__ __forceinline__ int split_at(int nu, int w) { return min(nu, (nu + 3) / 4 * w / FEW_NW * 4); }
+
 // What a wavefront does next.
 struct FewJob {
     int kind, g, at;                                   // group; first hidden feature (up) or column range (down)
 };
-enum { FEW_NONE = 0, FEW_IDLE = 1, FEW_UP_JOB = 2, FEW_DN_JOB = 3 };
+// FEW_SPLIT_JOB: an up job that the block's wavefronts share, each a part of K.
+enum { FEW_NONE = 0, FEW_IDLE = 1, FEW_UP_JOB = 2, FEW_SPLIT_JOB = 3, FEW_DN_JOB = 4 };
 
 template <int ST, bool X_LDS>
 __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
@@ -249,7 +272,6 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     uint16_t* s_grp = (uint16_t*)(s_tok + 1024);       // group of each selected expert
     if (tid < 64) s_ticket[tid] = 0;
     s_tok[tid] = s_tok[NT + tid] = 0;
-    __syncthreads();
     static_assert(2 * NT == 1024 && NT >= FEW_SLOTS, "two experts a thread, a slot a thread");
     for (int t = wave; t < T; t += FEW_NW) {
         int e;
@@ -259,9 +281,10 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
         if (lane < k) {
             s_idx[t * k + lane] = e;
             s_w[t * k + lane] = w;
-            atomicOr(&s_tok[e], 1u << t);
         }
     }
+    __syncthreads();
+    if (tid < slots) atomicOr(&s_tok[s_idx[tid]], 1u << (tid / k));
     __syncthreads();
     const uint32_t m0 = s_tok[2 * tid], m1 = s_tok[2 * tid + 1];
     int n_sel;
@@ -297,9 +320,15 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     if (tid == 0) s_ticket[0] = 1ull << 32 | (uint32_t)ticket;
     __syncthreads();
 
-    // ---- jobs.  Numbers of items [0, n_up): FEW_NW wavefronts' up jobs each; then ng * ncol down items.
+    // ---- jobs.  Numbers of items: n_wide items of FEW_NW wavefronts' up jobs each; then n_split up jobs that a block's
+    // wavefronts share; then ng * ncol down items.  Wide items run a block's wavefronts without a joint.  Where the
+    // up jobs are not a multiple of the grid's wavefronts, the rest of them as wide items would keep a few blocks
+    // busy (at the rate of a few CUs) while most wait for h: a rest of up to one job a block is shared out instead.
+    // (One token of the full layer: 2304 jobs on 2048 wavefronts.)
     const int ng = 1 + n_sel, nu_s = args.inter_s / FEW_UP, nu_r = args.inter / FEW_UP, ncol = d / FEW_DN;
-    const int n_wup = nu_s + n_sel * nu_r, n_up = (n_wup + FEW_NW - 1) / FEW_NW, total = n_up + ng * ncol;
+    const int n_wup = nu_s + n_sel * nu_r, rest = n_wup % (FEW_NW * (int)gridDim.x);
+    const int n_split = rest <= (int)gridDim.x ? rest : 0;
+    const int n_wide = (n_wup - n_split + FEW_NW - 1) / FEW_NW, n_up = n_wide + n_split, total = n_up + ng * ncol;
     int round = 0;                                     // of item numbers
     // The block's item of this round: its first lane leaves it in LDS, the other wavefronts find it there.  In the up
     // jobs wavefronts pass from round to round without waiting for each other; the barrier every 32 rounds (below)
@@ -310,10 +339,12 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
         const int item = __builtin_amdgcn_readfirstlane((int)got);
         if (item >= total) return {FEW_NONE, 0, 0};    // every block comes to a number past the end
         if (item >= n_up) return {FEW_DN_JOB, (item - n_up) / ncol, (item - n_up) % ncol};
-        const int it = item * FEW_NW + wave;
+        const bool wide = item < n_wide;
+        const int it = wide ? item * FEW_NW + wave : n_wup - n_split + item - n_wide;
         if (it >= n_wup) return {FEW_IDLE, 0, 0};
-        if (it < nu_s) return {FEW_UP_JOB, 0, it * FEW_UP};
-        return {FEW_UP_JOB, 1 + (it - nu_s) / nu_r, (it - nu_s) % nu_r * FEW_UP};
+        const int kind = wide ? FEW_UP_JOB : FEW_SPLIT_JOB;
+        if (it < nu_s) return {kind, 0, it * FEW_UP};
+        return {kind, 1 + (it - nu_s) / nu_r, (it - nu_s) % nu_r * FEW_UP};
     };
     Stream<ST, X_LDS, D> st;
     // The arguments are read anew for each job: kept over the loop they would take most scalar registers.
@@ -330,7 +361,7 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     // The stream goes on with this job's weights.
     auto start = [&](const FewJob& job) {
         const auto& a = *arguments();
-        if (job.kind == FEW_UP_JOB) {                  // eight rows of W1 and the same eight of W3
+        if (job.kind == FEW_UP_JOB || job.kind == FEW_SPLIT_JOB) {     // eight rows of W1 and the same eight of W3
             const int64_t ldw = (int64_t)d * 128 / LK;
             const int e = job.g ? __builtin_amdgcn_readfirstlane(s_exp[job.g]) : 0;
             const int64_t row0 = (int64_t)e * a.inter + job.at;
@@ -339,8 +370,10 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
                 s = (job.g ? (r16 < 8 ? a.W1s : a.W3s) : (r16 < 8 ? a.S1s : a.S3s)) + (row0 + (r16 & 7)) * (d / 32);
             if constexpr (ST == ST_FP8)                // the lane's results are of features 4 q .. 4 q + 3
                 s = (job.g ? (q < 2 ? a.W1s : a.W3s) : (q < 2 ? a.S1s : a.S3s)) + row0 / 128 * (d / 128) * 4;
+            const int nu = stream_units_of<ST>(d);
+            const bool all = job.kind == FEW_UP_JOB;
             st.start(weight_rows<ST>((job.g ? a.W1 : a.S1) + row0 * ldw, (job.g ? a.W3 : a.S3) + row0 * ldw, s, ldw, d, lane),
-                     stream_units_of<ST>(d));
+                     all ? 0 : split_at(nu, wave), all ? nu : split_at(nu, wave + 1));
             if constexpr (!X_LDS) {
                 int tok, slot, n;
                 up_rows(job, tok, slot, n);
@@ -355,12 +388,12 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
             if constexpr (ST == ST_MX4) s = (job.g ? a.W2s : a.S2s) + (row0 + r16) * (K / 32);
             if constexpr (ST == ST_FP8) s = (job.g ? a.W2s : a.S2s) + row0 / 128 * (K / 128) * 4;
             const uint8_t* p0 = (job.g ? a.W2 : a.S2) + row0 * ldw;
-            st.start(weight_rows<ST>(p0, p0 + 8 * ldw, s, ldw, K, lane), stream_units_of<ST>(K));
+            st.start(weight_rows<ST>(p0, p0 + 8 * ldw, s, ldw, K, lane), 0, stream_units_of<ST>(K));
             if constexpr (!X_LDS) st.ar = {a.x, a.xs, (uint32_t)(16 * q), 0, 0};       // travels along unused
         } else {
-            st.nu = 1;                                 // nothing follows: the last unit again, unused
+            st.stay();                                 // nothing follows: the last unit again, unused
         }
-        if constexpr (!X_LDS) st.ar_step = job.kind == FEW_UP_JOB;
+        if constexpr (!X_LDS) st.ar_step = job.kind == FEW_UP_JOB || job.kind == FEW_SPLIT_JOB;
     };
     auto next_job = [&]() -> FewJob {
         round++;
@@ -427,18 +460,32 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
         if (job.kind == FEW_IDLE) {
             then = next_job();
             filled = false;
-        } else if (job.kind == FEW_UP_JOB) {
+        } else if (job.kind != FEW_DN_JOB) {
             int tok, slot, n;
             up_rows(job, tok, slot, n);
-            const int nu = stream_units_of<ST>(d);
+            const bool split = job.kind == FEW_SPLIT_JOB;
+            const int nu = stream_units_of<ST>(d), u0 = split ? split_at(nu, wave) : 0, u1 = split ? split_at(nu, wave + 1) : nu;
             const ARows ax = {act, act_s, (uint32_t)tok * xstr + 16 * q, (uint32_t)tok * xsstr, st.wr.half};
-            int u = 0;
-            for (; u + D < nu; u += D) st.template round<true>(acc, ax, u, nu, 0, tiles[wave], lane);
+            int u = u0;
+            for (; u + D < u1; u += D) st.template round<true>(acc, ax, u, u1, 0, tiles[wave], lane);
             then = next_job();
             start(then);
-            st.template round<true>(acc, ax, u, nu, 0, tiles[wave], lane);
+            st.template round<true>(acc, ax, u, u1, 0, tiles[wave], lane);
             filled = then.kind != FEW_IDLE;
-            count_stored(nu <= D);
+            count_stored(u1 - u0 <= D);
+            if (split) {                               // the parts, joined in their order by the first wavefront
+                *(f32x4*)(tiles[wave] + lane * 16) = acc;
+                __syncthreads();
+                if (wave == 0) {
+#pragma unroll
+                    for (int w = 1; w < FEW_NW; w++) acc += *(const f32x4*)(tiles[w] + lane * 16);
+                }
+                __syncthreads();
+                if (wave) {
+                    job = then;
+                    continue;
+                }
+            }
             // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
             float hv[4];
 #pragma unroll
@@ -461,7 +508,7 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
             if (tid == 0) {
                 const int need = job.g ? nu_r : nu_s;
                 while (__hip_atomic_load(&a.up_done[job.g * FEW_PAD], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
-                    __builtin_amdgcn_s_sleep(4);
+                    __builtin_amdgcn_s_sleep(64);      // polls from every block delay the weights of those that work
                 s_last = count == ng - 1;
             }
             __syncthreads();                           // also: every wavefront is past the up jobs, x is not needed any more

@@ -85,7 +85,7 @@ __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
             *(uint32_t*)(xs + r * (XK / 32) + p * 4) = *(const uint32_t*)(bytes(g.As) + arow * g.ldas + k0 / 32 + p * 4);
         }
         if (k0 == 0) {                                 // behind the activations' loads, so that these do not wait for it
-            st.start(wr, nu);
+            st.start(wr, 0, nu);
             st.fill(lane);
         }
         lds_barrier();

@@ -178,22 +178,24 @@ template <int ST, bool A_LDS, int D> struct Stream {
     WRows wr;
     ARows ar;                                          // !A_LDS: the activations that travel along, and whether they
     int ar_step = 1;                                   // advance (0: the first unit again and again, unused)
-    int next, nu;                                      // the unit to load next; the matrix's units
+    int next, end;                                     // the unit to load next, and the first past those to load
 
-    __device__ __forceinline__ void start(const WRows& r, int units)
+    // Units [u0, u1) of these rows come next; u0 a multiple of SU.  (None: unit u0, if there is one, unused.)
+    __device__ __forceinline__ void start(const WRows& r, int u0, int u1)
     {
         wr = r;
-        next = 0;
-        nu = units;
+        next = u0;
+        end = u1;
     }
+    __device__ __forceinline__ void stay() { end = 1; }
     __device__ __forceinline__ void load(int j, int lane)
     {
-        const int u = min(next, nu - 1);
+        const int u = max(min(next, end - 1), 0);
         w[j].load(wr, u);
         if constexpr (ST == ST_MX4 || ST == ST_FP8) {
             if (j % SU == SU - 1) {                    // behind the last of the units it serves: the old words are used up
                 const int first = next - (SU - 1), i = ST == ST_MX4 ? 2 * first + (lane >> 4) : first + (lane & 3);
-                s[j / SU] = ((const uint32_t*)wr.s)[min(i, wr.ns - 1)];
+                s[j / SU] = ((const uint32_t*)wr.s)[max(min(i, wr.ns - 1), 0)];
             }
         }
         if constexpr (!A_LDS) a[j].load(ar, u * ar_step);
