@@ -17,10 +17,11 @@ int tile_rows(const moe_shape_t& s)
     // streaming).  Otherwise bf16 takes 256-row tiles: an expert of up to 256 rows reads its weights once,
     // and a 256 x 256 output block needs fewer staged bytes per MFMA than 128 x 512; row blocks past a
     // tile's end are skipped.  fp8 takes 256-row tiles above 192 rows per expert (fewer staged bytes and
-    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.  MXFP4 as fp8.
+    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.  MXFP4: 256, its kernel stages only the rows a
+    // tile has.
     const int64_t per_expert = s.T * s.k / (s.E > 0 ? s.E : 1);
     if (per_expert <= 24) return 16;
-    if (s.w_dtype == MOE_FP8_E4M3 || s.w_dtype == MOE_MXFP4) return per_expert > 192 ? 256 : 128;
+    if (s.w_dtype == MOE_FP8_E4M3) return per_expert > 192 ? 256 : 128;
     if (s.act_dtype == MOE_F32) return 128;
     return 256;
 }

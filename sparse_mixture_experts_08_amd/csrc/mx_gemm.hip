@@ -133,28 +133,44 @@ __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
 }
 
 // ---------------------------------------------------------------------------------------------------
-// 128- and 256-row tiles: eight wavefronts as 2 (rows) x 4 (features), operands and scales staged through LDS
-// by direct-to-LDS loads.  A K stage is 128 elements: 128 bytes of every activation row, 64 of every weight
-// row, and four scale bytes of each.  The 16-row blocks of a tile alternate between the two row groups of
-// wavefronts, so a tile that is not full still spreads over both.  A stage's LDS: BM rows of 128 bytes, NB rows
-// of 64 (both swizzled by row: see gemm.h), 512 scale words.
+// 256-row tiles.  Operands and scales are staged through LDS by direct-to-LDS loads; a K stage is 128 elements: 128
+// bytes of every activation row, 64 of every weight row (both swizzled by row: see gemm.h).  Activations are
+// staged 64 rows at a time, as many as the tile has, and what a stage leaves free becomes further stages of the
+// ring (three with 256 rows, six with 64).
+//
+// Scales are staged for four stages at once (SC16: 16 bytes of each row by one load; otherwise, where scale rows are
+// not whole 16-byte words, four planes of 4 bytes): one load of 4 bytes per row and stage fetched a
+// line per row each time and took as long as all the rest (the 4096-token layer 3.07 -> 2.44 ms without it).  A lane
+// turns them into one register per 16-row block that holds the stages' bytes; the instruction picks one.
+//
+// Eight wavefronts, 4 (rows) x 2 (features), two to a SIMD, which take turns: while one reads the fragments of a
+// stage into registers, the other one multiplies.  Barriers separate the turns, wavefronts 4-7 being one turn
+// behind.  Row blocks (16 rows) are dealt to the row groups in turn, so a short tile still spreads over all.
 // ---------------------------------------------------------------------------------------------------
-template <bool UP, int BM, int BN, int NSTG>
+constexpr int MX_BM = 256, MX_RING = 3 * (MX_BM * 128 + 256 * 64);
+
+// Byte offset of 16-byte chunk c of LDS row r, of 128 and of 64 bytes.  A 16-byte read takes 16 lanes a clock: lanes
+// 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31, and so on.  With lane = row + 16 chunk that is half of the 16 rows
+// at one chunk and the other half at the next, which these orders place on all 64 banks.  (gemm.h's order is made for
+// 32 rows at one chunk; with it 45 % of the reads' clocks were conflicts and the down GEMM of
+// 16384 tokens took 2.49 instead of 1.99 ms.)
+__device__ __forceinline__ int mx_swz128(int r, int c) { return r * 128 + ((c ^ (r >> 1 & 7)) << 4); }
+__device__ __forceinline__ int mx_swz64(int r, int c) { return r * 64 + ((c ^ (r >> 2 & 3)) << 4); }
+
+template <bool UP, int BN, bool SC16>
 __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
 {
+    constexpr int BM = MX_BM;
     constexpr int NB = UP ? 2 * BN : BN;               // weight rows per stage
-    constexpr int WM = BM / 32, WN = BN / 64;          // 16-row and 16-feature blocks per wavefront
-    constexpr int PA = BM / 64, PB = NB / 128;         // 1-KB loads per wavefront and stage: activations, weights
-    constexpr int NL = PA + PB + 1;                    // ... and one load of scales
-    constexpr int STAGE = BM * 128 + NB * 64;
-    static_assert(BM == 128 || BM == 256, "128- or 256-row tiles");
-    static_assert(!UP || BN == 128, "a wavefront's 32 features of h are one group");
-    static_assert(BM / 64 <= 4 && NB / 64 <= 4, "wavefronts 0-3 copy activation scales, 4-7 weight scales");
-    static_assert((NSTG - 1) * NL < 64, "vmcnt range");
+    constexpr int WM = BM / 64, WB = NB / 32;          // 16-row blocks per wavefront: activations, weights
+    constexpr int WN = BN / 32;                        // ... of one matrix
+    constexpr int PB = NB / 128;                       // 1-KB loads of weights per wavefront and stage
+    static_assert(!UP || BN == 128, "a wavefront has 64 features of h");
+    static_assert(NB == 128 || NB == 256, "whole loads, and scales of 256 + NB rows");
     constexpr int OSTR = (UP ? BN : BN * 2) + 16;      // epilogue: padded LDS row of the output tile
-    constexpr int RING = NSTG * STAGE > BM * OSTR ? NSTG * STAGE : BM * OSTR;
-    __shared__ __attribute__((aligned(1024))) uint8_t ring[RING];
-    __shared__ __attribute__((aligned(256))) uint32_t scl[NSTG][512];
+    static_assert(BM * OSTR <= MX_RING, "the output tile replaces the stages");
+    __shared__ __attribute__((aligned(1024))) uint8_t ring[MX_RING];
+    __shared__ __attribute__((aligned(1024))) uint8_t scl[512 * 16];   // SC16: [row][stage % 4], else [stage % 4][row]
     __shared__ int s_tok[BM];
 
     int tile, nb;
@@ -167,7 +183,8 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
     if (n0 >= N) return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int mg = wave >> 2, ng = wave & 3;           // row group, feature group
+    // wavefronts w and w + 4 share a SIMD: row groups 0 and 3, or 1 and 2
+    const int late = wave >> 2, mg = late ? 3 - (wave & 1) : wave & 1, ng = (wave >> 1) & 1;
     const int r16 = lane & 15, q = lane >> 4;
     const MxGroup m = mx_group<UP>(g, grp, shared, N, K);
 
@@ -178,133 +195,176 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
     // Sources, fixed over the K walk (32-bit offsets: the host keeps every operand under 4 GB).  Lane l of a load
     // writes 16-byte chunk l % 8 of row l / 8 (activations) or l % 4 of row l / 4 (weights) and so reads the
     // logical chunk that the swizzle keeps there.
-    uint32_t offA[PA], offB[PB];
+    uint32_t offA[WM], offB[PB];
 #pragma unroll
-    for (int p = 0; p < PA; p++) {
+    for (int p = 0; p < WM; p++) {
         const int row = (p * 8 + wave) * 8 + (lane >> 3);
-        offA[p] = (uint32_t)s_tok[row] * (uint32_t)g.lda + (swzr<128>(row, lane & 7) - row * 128);
+        offA[p] = (uint32_t)s_tok[row] * (uint32_t)g.lda + (mx_swz128(row, lane & 7) - row * 128);
     }
 #pragma unroll
     for (int p = 0; p < PB; p++) {
         const int row = (p * 8 + wave) * 16 + (lane >> 2);             // UP: rows BN .. are W3's
-        offB[p] = (uint32_t)(n0 + (UP ? row % BN : row)) * (uint32_t)m.ldb + (swzr<64>(row, lane & 3) - row * 64);
+        offB[p] = (uint32_t)(n0 + (UP ? row % BN : row)) * (uint32_t)m.ldb + (mx_swz64(row, lane & 3) - row * 64);
     }
-    // Scale words in the order the wavefronts read them: activations of row group mg at mg BM / 2 + 64 v + 4 r16 +
-    // e = row 16 (2 (4 v + e) + mg) + r16; weights of feature group ng, matrix by matrix, at 16 WN ng + WN r16 + e
-    // = feature 16 WN ng + 16 e + r16.
-    uint32_t offS = 0;
-    const uint8_t* baseS = bytes(g.As);
+    // scales: wavefronts 0-3 the activation rows', 4-7 the weight rows' (NB = 128: 6 and 7 repeat 4 and 5)
+    uint32_t offS;
+    const uint8_t* baseS;
     if (wave < 4) {
-        const int p = (wave * 64 + lane) % BM, rem = p % (BM / 2);     // BM = 128: wavefronts 2, 3 repeat 0, 1
-        const int row = 16 * (2 * (4 * (rem / 64) + rem % 4) + p / (BM / 2)) + (rem % 64) / 4;
-        offS = (uint32_t)s_tok[row] * (uint32_t)g.ldas;
+        offS = (uint32_t)s_tok[wave * 64 + lane] * (uint32_t)g.ldas;
+        baseS = bytes(g.As);
     } else {
-        const int p = ((wave - 4) * 64 + lane) % NB, f = p % BN, rem = f % (16 * WN);
-        const int row = f - rem + 16 * (rem % WN) + rem / WN;
-        offS = (uint32_t)(n0 + row) * (uint32_t)m.nkb;
+        const int row = ((wave - 4) * 64 + lane) % NB;
+        offS = (uint32_t)(n0 + row % BN) * (uint32_t)m.nkb;
         baseS = UP && ((wave - 4) * 64) % NB >= BN ? m.W3s : m.W1s;    // BN is a multiple of 64: wave-uniform
     }
-
     const int nstages = K / 128;
-    const int kshift = (nb * g.krot) % nstages;
-    const uint32_t ring0 = lds_addr(ring), scl0 = lds_addr(&scl[0][0]);
-    auto issue = [&](int buf, int s) {
-        const int ks = s + kshift >= nstages ? s + kshift - nstages : s + kshift;
-        const uint32_t dst = ring0 + buf * STAGE + wave * 1024;
+    const uint32_t ring0 = lds_addr(ring), scl0 = lds_addr(scl);
+    auto issue_scales = [&](int c) {                   // of stages 4 c .. 4 c + 3; past the end: the last again
+        if constexpr (SC16) dma16(baseS + (int64_t)min(c, (nstages - 1) / 4) * 16, offS, scl0 + wave * 1024);
+        else
 #pragma unroll
-        for (int p = 0; p < PA; p++) dma16(g.A + (int64_t)ks * 128, offA[p], dst + p * 8192);
-#pragma unroll
-        for (int p = 0; p < PB; p++)
-            dma16((UP && p * 128 >= BN ? m.W3 : m.W1) + (int64_t)ks * 64, offB[p], dst + BM * 128 + p * 8192);
-        dma4(baseS + (int64_t)ks * 4, offS, scl0 + (buf * 512 + wave * 64) * 4);
+            for (int j = 0; j < 4; j++)
+                dma4(baseS + (int64_t)min(4 * c + j, nstages - 1) * 4, offS, scl0 + j * 2048 + wave * 256);
     };
 
-    f32x4 acc1[WM][WN], acc3[WM][UP ? WN : 1];
+    f32x4 acc[WM][WB];                                 // UP: features of W1, then of W3
 #pragma unroll
-    for (int i = 0; i < WM; i++) {
+    for (int i = 0; i < WM; i++)
 #pragma unroll
-        for (int j = 0; j < WN; j++) acc1[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int j = 0; j < (UP ? WN : 1); j++) acc3[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
-    }
-    // 16-row blocks of this wavefront that hold tile rows (wave-uniform): i with 16 (2 i + mg) < rows
-    const int nrb = __builtin_amdgcn_readfirstlane(max(0, min(WM, ((rows + 15) / 16 - mg + 1) / 2)));
+        for (int j = 0; j < WB; j++) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
+    // Fragments in a stage: the row blocks of a wavefront are multiples of 16 rows apart, and the orders repeat
+    // every 16 rows.
+    const int a_lo = mx_swz128(16 * mg + r16, q), a_hi = mx_swz128(16 * mg + r16, 4 + q);
+    const int w_at = mx_swz64(ng * (BN / 2) + r16, q);
+    constexpr int SROW = SC16 ? 16 : 4;                // bytes between rows' scales
+    const int a_sc = (16 * mg + r16) * SROW, w_sc = (BM + ng * (BN / 2) + r16) * SROW;
 
-    auto k_walk = [&](auto nb_tag) {
-        constexpr int NR = decltype(nb_tag)::value;
+    auto k_walk = [&](auto nr_tag) {
+        constexpr int NR = decltype(nr_tag)::value;    // 64-row steps of the tile
+        if constexpr (NR > 0) {
+            constexpr int STAGE = NR * 8192 + NB * 64, FIT = MX_RING / STAGE, NSTG = FIT < 6 ? FIT : 6;
+            constexpr int NL = NR + PB;                // loads per wavefront and stage
+            static_assert(NSTG >= 3 && (NSTG - 2) * NL < 64, "two stages ahead; vmcnt range");
+            const bool last = 16 * (4 * (NR - 1) + mg) < rows;         // the last step's block has rows (wave-uniform)
+            auto issue = [&](int buf, int s) {
+                const uint32_t dst = ring0 + buf * STAGE + wave * 1024;
+                const int ks = min(s, nstages - 1);    // past the end: the last stage again (never read)
 #pragma unroll
-        for (int t = 0; t < NSTG; t++) issue(t, min(t, nstages - 1));
-        wait_vmcnt<(NSTG - 1) * NL>();
-        lds_barrier();
-        int buf = 0;
-        for (int s = 0; s < nstages; s++) {
-            const uint8_t* sa = ring + buf * STAGE;
-            const uint8_t* sb = sa + BM * 128;
-            const uint32_t* sc = scl[buf];
-            if constexpr (NR > 0) {
-                i32x8 b1[WN], b3[UP ? WN : 1];
-                uint32_t s1[WN], s3[UP ? WN : 1], as[WM];
-                auto wfrag = [&](int row) {
-                    const i32x4 lo = *(const i32x4*)(sb + swzr<64>(row, q));
-                    return (i32x8){lo.x, lo.y, lo.z, lo.w, 0, 0, 0, 0};
-                };
+                for (int p = 0; p < NR; p++) dma16(g.A + (int64_t)ks * 128, offA[p], dst + p * 8192);
 #pragma unroll
-                for (int j = 0; j < WN; j++) {
-                    b1[j] = wfrag(ng * 16 * WN + 16 * j + r16);
-                    s1[j] = sc[256 + ng * 16 * WN + r16 * WN + j] >> (8 * q);
-                    if constexpr (UP) {
-                        b3[j] = wfrag(BN + ng * 16 * WN + 16 * j + r16);
-                        s3[j] = sc[256 + BN + ng * 16 * WN + r16 * WN + j] >> (8 * q);
-                    }
+                for (int p = 0; p < PB; p++)
+                    dma16((UP && p * 128 >= BN ? m.W3 : m.W1) + (int64_t)ks * 64, offB[p], dst + NR * 8192 + p * 8192);
+            };
+            uint32_t as[NR], ws[WB];
+            // One stage.  Its fragments are read in the first turn; the loads issued there go to the buffer of the
+            // stage before, which every wavefront has read (the other half in the turn before this one).  Before
+            // wavefronts 0-3 begin on the next stage it has landed for all: what may still be on its way then is
+            // the NSTG - 2 stages behind it.  That moment is the end of their own second turn and of the others'
+            // first.  Scales are read at the first of four stages and loaded again at the second, by when
+            // both halves have read them; at the fourth, when they must be there, two stages' loads are younger.
+            auto stage = [&](auto j_tag, int s, int& buf) {
+                constexpr int J = decltype(j_tag)::value;
+                constexpr int BEHIND = (J == 3 && NSTG > 4 ? 2 : NSTG - 2) * NL;
+                const uint8_t* sa = ring + buf * STAGE;
+                const uint8_t* sb = sa + NR * 8192;
+                if constexpr (J == 0) {
+                    const uint32_t sel = 0x0c0c0400u + 0x0101u * (uint32_t)q;  // byte q of two words
+                    auto gather = [&](const uint8_t* p) {
+                        uint32_t w[4];
+                        if constexpr (SC16) {
+                            const uint4 v = *(const uint4*)p;
+                            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; e++) w[e] = *(const uint32_t*)(p + e * 2048);
+                        }
+                        return __builtin_amdgcn_perm(w[1], w[0], sel) | __builtin_amdgcn_perm(w[3], w[2], sel) << 16;
+                    };
+#pragma unroll
+                    for (int i = 0; i < NR; i++) as[i] = gather(scl + a_sc + 64 * i * SROW);
+#pragma unroll
+                    for (int j = 0; j < WB; j++) ws[j] = gather(scl + w_sc + ((j / WN) * BN + 16 * (j % WN)) * SROW);
                 }
+                i32x4 b[WB];
+                i32x8 a[NR];
 #pragma unroll
-                for (int i = 0; i < NR; i++) as[i] = sc[mg * (BM / 2) + 64 * (i / 4) + 4 * r16 + i % 4] >> (8 * q);
+                for (int j = 0; j < WB; j++)
+                    b[j] = *(const i32x4*)(sb + w_at + ((j / WN) * BN + 16 * (j % WN)) * 64);
 #pragma unroll
                 for (int i = 0; i < NR; i++) {
-                    const int row = 16 * (2 * i + mg) + r16;
-                    const i32x4 lo = *(const i32x4*)(sa + swzr<128>(row, q));
-                    const i32x4 hi = *(const i32x4*)(sa + swzr<128>(row, 4 + q));
-                    const i32x8 a = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                    const i32x4 lo = *(const i32x4*)(sa + a_lo + 64 * i * 128), hi = *(const i32x4*)(sa + a_hi + 64 * i * 128);
+                    a[i] = (i32x8){lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                }
+                issue(buf == 0 ? NSTG - 1 : buf - 1, s + NSTG - 1);
+                if constexpr (J == 1) issue_scales(s / 4 + 1);
+                if (late) wait_vmcnt<BEHIND>();
+                lds_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+                __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-                    for (int j = 0; j < WN; j++) {
-                        acc1[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b1[j], a, acc1[i][j], 4, 0, 0, (int)s1[j], 0, (int)as[i]);
-                        if constexpr (UP)
-                            acc3[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b3[j], a, acc3[i][j], 4, 0, 0, (int)s3[j], 0, (int)as[i]);
+                for (int i = 0; i < NR; i++) {
+                    if (i < NR - 1 || last) {
+#pragma unroll
+                        for (int j = 0; j < WB; j++) {
+                            const i32x8 w = {b[j].x, b[j].y, b[j].z, b[j].w, 0, 0, 0, 0};
+                            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a[i], acc[i][j], 4, 0, J, (int)ws[j], J, (int)as[i]);
+                        }
                     }
                 }
-            }
-            if (s + 1 < nstages) {
-                wait_vmcnt<(NSTG - 2) * NL>();         // stage s + 1 has landed
-                lds_barrier();                         // ... for every wavefront, and stage s is read
-                issue(buf, min(s + NSTG, nstages - 1)); // past the end: the last stage again (never read)
+#pragma unroll
+                for (int i = 0; i < NR; i++)
+#pragma unroll
+                    for (int j = 0; j < WB; j++) asm volatile("" : "+v"(acc[i][j]));   // the products stay in this turn
+                __builtin_amdgcn_s_setprio(0);
+                __builtin_amdgcn_sched_barrier(0);
+                if (!late) wait_vmcnt<BEHIND>();
+                lds_barrier();
                 buf = buf + 1 == NSTG ? 0 : buf + 1;
+            };
+            issue_scales(0);
+#pragma unroll
+            for (int t = 0; t < NSTG - 1; t++) issue(t, t);
+            wait_vmcnt<(NSTG - 2) * NL>();
+            lds_barrier();
+            if (late) lds_barrier();                   // half a stage behind
+            int buf = 0;
+            for (int s = 0; s < nstages; s += 4) {
+                stage(IntC<0>{}, s, buf);
+                if (s + 1 < nstages) stage(IntC<1>{}, s + 1, buf);
+                if (s + 2 < nstages) stage(IntC<2>{}, s + 2, buf);
+                if (s + 3 < nstages) stage(IntC<3>{}, s + 3, buf);
             }
+            if (!late) lds_barrier();
         }
     };
-    with_count<WM>(nrb, k_walk);
+    with_count<WM>(__builtin_amdgcn_readfirstlane((rows + 63) / 64), k_walk);
     wait_vmcnt<0>();                                   // no load may still target this block's LDS
     lds_barrier();
 
     if constexpr (UP) {
-        // h of a token's 32 features (this wavefront's) lies on the four lanes r16 + 16 q, eight values each
+        // h of a token's 32 features lies on the four lanes r16 + 16 q, eight values each
 #pragma unroll
         for (int i = 0; i < WM; i++) {
-            const int row = 16 * (2 * i + mg) + r16;
-            float v[8];
+            const int row = 16 * (4 * i + mg) + r16;
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                float gg = acc1[i][e / 4][e % 4], uu = acc3[i][e / 4][e % 4];
-                round_bf16x2(gg, uu);
-                v[e] = round_bf16(silu_mul_fast(gg, uu));
+            for (int p = 0; p < WN / 2; p++) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; e++) {
+                    float gg = acc[i][2 * p + e / 4][e % 4], uu = acc[i][WN + 2 * p + e / 4][e % 4];
+                    round_bf16x2(gg, uu);
+                    v[e] = round_bf16(silu_mul_fast(gg, uu));
+                }
+                uint32_t am = mx_amax8(v);
+                am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
+                am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
+                const uint32_t c = mx_scale_code<false>(am);
+                const uint2 pk = c == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(v, c);
+                const int f = ng * 64 + p * 32;
+                *(uint32_t*)(ring + row * OSTR + f + 4 * q) = pk.x;
+                *(uint32_t*)(ring + row * OSTR + f + 16 + 4 * q) = pk.y;
+                if (q == 0 && row < rows) ((uint8_t*)g.outs)[((int64_t)row0 + row) * g.ldos + (n0 + f) / 32] = (uint8_t)c;
             }
-            uint32_t am = mx_amax8(v);
-            am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
-            am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
-            const uint32_t c = mx_scale_code<false>(am);
-            const uint2 p = c == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(v, c);
-            *(uint32_t*)(ring + row * OSTR + ng * 32 + 4 * q) = p.x;
-            *(uint32_t*)(ring + row * OSTR + ng * 32 + 16 + 4 * q) = p.y;
-            if (q == 0 && row < rows) ((uint8_t*)g.outs)[((int64_t)row0 + row) * g.ldos + n0 / 32 + ng] = (uint8_t)c;
         }
         __syncthreads();
         constexpr int CH = BN / 16;
@@ -317,10 +377,10 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
 #pragma unroll
         for (int i = 0; i < WM; i++)
 #pragma unroll
-            for (int j = 0; j < WN; j++) {
-                const uint32_t lo = f32x2_to_bf16x2(acc1[i][j][0], acc1[i][j][1]);
-                const uint32_t hi = f32x2_to_bf16x2(acc1[i][j][2], acc1[i][j][3]);
-                *(uint2*)(ring + (16 * (2 * i + mg) + r16) * OSTR + (ng * 16 * WN + j * 16 + 4 * q) * 2) = make_uint2(lo, hi);
+            for (int j = 0; j < WB; j++) {
+                const uint32_t lo = f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]);
+                const uint32_t hi = f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]);
+                *(uint2*)(ring + (16 * (4 * i + mg) + r16) * OSTR + (ng * (BN / 2) + j * 16 + 4 * q) * 2) = make_uint2(lo, hi);
             }
         __syncthreads();
         store_tile_bf16<BM, BN, OSTR, 512, true>(ring, g.out, g.ldo, row0, rows, n0);
@@ -330,20 +390,20 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
 template <bool UP>
 static void launch_mx(const moe_shape_t& s, GemmArgs a, int N, hipStream_t stream)
 {
-    const int bm = tile_rows(s);
     const bool wide = !UP && N % 256 == 0;             // down: 256-wide n-blocks where d allows
-    a.n_blocks = bm == 16 && !UP ? (N + 255) / 256 : N / (wide ? 256 : 128);
+    const bool few = tile_rows(s) == 16;
+    a.n_blocks = few && !UP ? (N + 255) / 256 : N / (wide ? 256 : 128);
     const unsigned grid = (unsigned)launch_blocks(a);
-    if (bm == 16) mx_gemm_stream_kernel<UP><<<grid, 1024, 0, stream>>>(a);
-    else if constexpr (UP) {
-        if (bm == 128) mx_gemm_kernel<true, 128, 128, 4><<<grid, 512, 0, stream>>>(a);
-        else mx_gemm_kernel<true, 256, 128, 3><<<grid, 512, 0, stream>>>(a);
-    } else if (wide) {
-        if (bm == 128) mx_gemm_kernel<false, 128, 256, 4><<<grid, 512, 0, stream>>>(a);
-        else mx_gemm_kernel<false, 256, 256, 3><<<grid, 512, 0, stream>>>(a);
-    } else {
-        if (bm == 128) mx_gemm_kernel<false, 128, 128, 4><<<grid, 512, 0, stream>>>(a);
-        else mx_gemm_kernel<false, 256, 128, 3><<<grid, 512, 0, stream>>>(a);
+    // scale rows in 16-byte words: of both operands, of routed and shared groups
+    const uintptr_t at = (uintptr_t)a.As | (uintptr_t)a.B1s | (uintptr_t)a.B3s | (uintptr_t)a.S1s | (uintptr_t)a.S3s;
+    const bool sc16 = ((at | (uintptr_t)a.ldas | (uintptr_t)(a.K_r / 32) | (uintptr_t)(a.S1s ? a.K_s / 32 | a.nkb_s : 0)) & 15) == 0;
+    if (few) mx_gemm_stream_kernel<UP><<<grid, 1024, 0, stream>>>(a);
+    else if (UP || !wide) {
+        if (sc16) mx_gemm_kernel<UP, 128, true><<<grid, 512, 0, stream>>>(a);
+        else mx_gemm_kernel<UP, 128, false><<<grid, 512, 0, stream>>>(a);
+    } else if constexpr (!UP) {
+        if (sc16) mx_gemm_kernel<false, 256, true><<<grid, 512, 0, stream>>>(a);
+        else mx_gemm_kernel<false, 256, false><<<grid, 512, 0, stream>>>(a);
     }
 }
 
@@ -355,7 +415,7 @@ static GemmArgs mx_args(const moe_shape_t& s, const Workspace& ws, int e_base)
     a.ntiles = ws.sync;
     a.max_tiles = (int)ws.max_tiles;
     a.E = (int)s.E;
-    a.group_m = tile_rows(s) == 16 ? 0 : 4;
+    a.group_m = tile_rows(s) == 16 ? 0 : 2;
     return a;
 }
 
