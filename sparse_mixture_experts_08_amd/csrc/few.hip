@@ -39,6 +39,10 @@ constexpr int FEW_NW = 8;                              // wavefronts per block o
 constexpr int FEW_UP = 8;                              // hidden features a wavefront in an up item
 constexpr int FEW_DN = 16 * FEW_NW;                    // output features per down item
 constexpr int FEW_PAD = 16;                            // ints between counters: a 64-byte line each
+// A group's up jobs are counted in FEW_SUB places: 256 additions to one address at a time take 2 - 5 us in turn (one
+// MXFP4 token 66 us with one place, 65 with four or eight; the smallest layer loses to the longer polls with
+// more: 30.0 us with eight, 33.7 with 32).
+constexpr int FEW_SUB = 4;
 
 struct FewArgs {
     int T, d, E, k, inter, inter_s, inter_max;
@@ -51,7 +55,7 @@ struct FewArgs {
     uint8_t* y_rows;                                   // [T k + T, d] act dtype
     uint8_t* y;
     int32_t *idx_out, *w_out_bits, *counts_out;        // optional
-    int32_t *ticket, *up_done, *col_done;              // counters: [1], [FEW_GROUPS], [d / FEW_DN], FEW_PAD apart
+    int32_t *ticket, *up_done, *col_done;              // counters: [1], [FEW_GROUPS][FEW_SUB], [d / FEW_DN], FEW_PAD apart
 };
 
 // ---------------------------------------------------------------------------------------------------
@@ -190,8 +194,11 @@ __device__ __forceinline__ uint4 get128(const void* p)
     const u64 a = get64(p), b = get64((const uint8_t*)p + 8);
     return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)b, (uint32_t)(b >> 32));
 }
+// By one lane.  The address is a lane's own as far as the compiler knows: for one that is the wavefront's it adds up
+// the lanes first and waits at once for the result, and so for every load of weights before it.
 __device__ __forceinline__ int32_t bump(int32_t* counter)
 {
+    asm volatile("" : "+v"(counter));
     return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 // Four consecutive values, rounded to bf16 or as they are.
@@ -247,7 +254,7 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     __shared__ uint8_t s_n[FEW_GROUPS];
     __shared__ uint8_t s_slot[FEW_GROUPS][16];         // the slots of a group's rows (group 0, the shared one: tokens)
     __shared__ volatile uint64_t s_ticket[64];         // round + 1 and the item number taken for it, by round % 64
-    __shared__ int scan[FEW_NW + 1];
+    __shared__ int scan[FEW_NW];                       // selected experts of a wavefront's 128
     __shared__ int s_last;
 
     const int tid = threadIdx.x, lane = tid & 63;
@@ -258,94 +265,6 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     const int xsstr = ST == ST_MX4 ? d / 32 : ST == ST_FP8 ? d / 128 * 4 : 0;   // ... of its scales
     int ticket = 0;
     if (tid == 0) ticket = bump(args.ticket);
-
-    // ---- x into LDS, and the selection: every block for itself
-    if constexpr (X_LDS) {
-        const int vecs = d * XB / 16;                  // 16-byte vectors a row
-        for (int i = tid; i < T * vecs; i += NT) {
-            const int t = i / vecs;
-            *(uint4*)(act + t * xstr + (i - t * vecs) * 16) = ((const uint4*)args.x)[i];
-        }
-        for (int i = tid; i < T * xsstr / 4; i += NT) ((uint32_t*)act_s)[i] = ((const uint32_t*)args.xs)[i];
-    }
-    uint32_t* s_tok = (uint32_t*)tiles;                // tokens (bits) of each expert
-    uint16_t* s_grp = (uint16_t*)(s_tok + 1024);       // group of each selected expert
-    if (tid < 64) s_ticket[tid] = 0;
-    s_tok[tid] = s_tok[NT + tid] = 0;
-    static_assert(2 * NT == 1024 && NT >= FEW_SLOTS, "two experts a thread, a slot a thread");
-    for (int t = wave; t < T; t += FEW_NW) {
-        int e;
-        float w;
-        if (E <= 256) topk_group<64, 4>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
-        else topk_group<64, 16>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
-        if (lane < k) {
-            s_idx[t * k + lane] = e;
-            s_w[t * k + lane] = w;
-        }
-    }
-    __syncthreads();
-    if (tid < slots) atomicOr(&s_tok[s_idx[tid]], 1u << (tid / k));
-    __syncthreads();
-    const uint32_t m0 = s_tok[2 * tid], m1 = s_tok[2 * tid + 1];
-    int n_sel;
-    const int rank = 1 + block_exclusive_scan<NT>((m0 != 0) + (m1 != 0), &n_sel, scan);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const uint32_t m = i ? m1 : m0;
-        const int r = i ? rank + (m0 != 0) : rank;
-        if (m) {
-            s_grp[2 * tid + i] = (uint16_t)r;
-            s_exp[r] = (uint16_t)(2 * tid + i);
-            s_n[r] = (uint8_t)__popc(m);
-        }
-    }
-    if (tid < 16) s_slot[0][tid] = (uint8_t)min(tid, T - 1);
-    if (tid == 0) s_n[0] = (uint8_t)T;
-    __syncthreads();
-    if (tid < slots) {
-        const int t = tid / k, e = s_idx[tid];
-        s_slot[s_grp[e]][__popc(s_tok[e] & ((1u << t) - 1u))] = (uint8_t)tid;
-        int before = 0;
-        for (int j = 0; j < k; j++) before += s_idx[t * k + j] < e;
-        s_order[t * k + before] = (uint8_t)tid;
-    }
-    if (blockIdx.x == 0) {
-        if (tid < slots) {
-            if (args.idx_out) args.idx_out[tid] = s_idx[tid];
-            if (args.w_out_bits) args.w_out_bits[tid] = __float_as_int(s_w[tid]);
-        }
-        if (args.counts_out)
-            for (int e = tid; e < E; e += NT) args.counts_out[e] = __popc(s_tok[e]);
-    }
-    if (tid == 0) s_ticket[0] = 1ull << 32 | (uint32_t)ticket;
-    __syncthreads();
-
-    // ---- jobs.  Numbers of items: n_wide items of FEW_NW wavefronts' up jobs each; then n_split up jobs that a block's
-    // wavefronts share; then ng * ncol down items.  Wide items run a block's wavefronts without a joint.  Where the
-    // up jobs are not a multiple of the grid's wavefronts, the rest of them as wide items would keep a few blocks
-    // busy (at the rate of a few CUs) while most wait for h: a rest of up to one job a block is shared out instead.
-    // (One token of the full layer: 2304 jobs on 2048 wavefronts.)
-    const int ng = 1 + n_sel, nu_s = args.inter_s / FEW_UP, nu_r = args.inter / FEW_UP, ncol = d / FEW_DN;
-    const int n_wup = nu_s + n_sel * nu_r, rest = n_wup % (FEW_NW * (int)gridDim.x);
-    const int n_split = rest <= (int)gridDim.x ? rest : 0;
-    const int n_wide = (n_wup - n_split + FEW_NW - 1) / FEW_NW, n_up = n_wide + n_split, total = n_up + ng * ncol;
-    int round = 0;                                     // of item numbers
-    // The block's item of this round: its first lane leaves it in LDS, the other wavefronts find it there.  In the up
-    // jobs wavefronts pass from round to round without waiting for each other; the barrier every 32 rounds (below)
-    // keeps the fastest from overwriting a number that the slowest has not read.
-    auto job_of_round = [&]() -> FewJob {
-        uint64_t got;
-        while ((int)((got = s_ticket[round % 64]) >> 32) != round + 1) __builtin_amdgcn_s_sleep(1);
-        const int item = __builtin_amdgcn_readfirstlane((int)got);
-        if (item >= total) return {FEW_NONE, 0, 0};    // every block comes to a number past the end
-        if (item >= n_up) return {FEW_DN_JOB, (item - n_up) / ncol, (item - n_up) % ncol};
-        const bool wide = item < n_wide;
-        const int it = wide ? item * FEW_NW + wave : n_wup - n_split + item - n_wide;
-        if (it >= n_wup) return {FEW_IDLE, 0, 0};
-        const int kind = wide ? FEW_UP_JOB : FEW_SPLIT_JOB;
-        if (it < nu_s) return {kind, 0, it * FEW_UP};
-        return {kind, 1 + (it - nu_s) / nu_r, (it - nu_s) % nu_r * FEW_UP};
-    };
     Stream<ST, X_LDS, D> st;
     // The arguments are read anew for each job: kept over the loop they would take most scalar registers.
     auto arguments = [&]() -> KernArgs {
@@ -395,12 +314,109 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
         }
         if constexpr (!X_LDS) st.ar_step = job.kind == FEW_UP_JOB || job.kind == FEW_SPLIT_JOB;
     };
+
+    // ---- x into LDS, and the selection: every block for itself
+    if constexpr (X_LDS) {
+        const int vecs = d * XB / 16;                  // 16-byte vectors a row
+        for (int i = tid; i < T * vecs; i += NT) {
+            const int t = i / vecs;
+            *(uint4*)(act + t * xstr + (i - t * vecs) * 16) = ((const uint4*)args.x)[i];
+        }
+        for (int i = tid; i < T * xsstr / 4; i += NT) ((uint32_t*)act_s)[i] = ((const uint32_t*)args.xs)[i];
+    }
+    uint32_t* s_tok = (uint32_t*)tiles;                // tokens (bits) of each expert
+    uint16_t* s_grp = (uint16_t*)(s_tok + 1024);       // group of each selected expert
+    if (tid < 64) s_ticket[tid] = 0;
+    s_tok[tid] = s_tok[NT + tid] = 0;
+    static_assert(2 * NT == 1024 && NT >= FEW_SLOTS, "two experts a thread, a slot a thread");
+    for (int t = wave; t < T; t += FEW_NW) {
+        int e;
+        float w;
+        if (E <= 256) topk_group<64, 4>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
+        else topk_group<64, 16>(args.logits + (size_t)t * E, nullptr, E, k, lane, e, w);
+        if (lane < k) {
+            s_idx[t * k + lane] = e;
+            s_w[t * k + lane] = w;
+        }
+    }
+    lds_barrier();
+    if (tid < slots) atomicOr(&s_tok[s_idx[tid]], 1u << (tid / k));
+    lds_barrier();
+    const uint32_t m0 = s_tok[2 * tid], m1 = s_tok[2 * tid + 1];
+    // groups 1 ..: the selected experts in ascending order
+    const uint64_t b0 = __ballot(m0 != 0), b1 = __ballot(m1 != 0), below = (1ull << lane) - 1;
+    if (lane == 0) scan[wave] = __popcll(b0) + __popcll(b1);
+    lds_barrier();
+    int n_sel = 0, rank = 1 + __popcll(b0 & below) + __popcll(b1 & below);
+#pragma unroll
+    for (int w = 0; w < FEW_NW; w++) {
+        rank += w < wave ? scan[w] : 0;
+        n_sel += scan[w];
+    }
+    n_sel = __builtin_amdgcn_readfirstlane(n_sel);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const uint32_t m = i ? m1 : m0;
+        const int r = i ? rank + (m0 != 0) : rank;
+        if (m) {
+            s_grp[2 * tid + i] = (uint16_t)r;
+            s_exp[r] = (uint16_t)(2 * tid + i);
+            s_n[r] = (uint8_t)__popc(m);
+        }
+    }
+    if (tid < 16) s_slot[0][tid] = (uint8_t)min(tid, T - 1);
+    if (tid == 0) s_n[0] = (uint8_t)T;
+    lds_barrier();
+    if (tid < slots) {
+        const int t = tid / k, e = s_idx[tid];
+        s_slot[s_grp[e]][__popc(s_tok[e] & ((1u << t) - 1u))] = (uint8_t)tid;
+        int before = 0;
+        for (int j = 0; j < k; j++) before += s_idx[t * k + j] < e;
+        s_order[t * k + before] = (uint8_t)tid;
+    }
+    if (blockIdx.x == 0) {
+        if (tid < slots) {
+            if (args.idx_out) args.idx_out[tid] = s_idx[tid];
+            if (args.w_out_bits) args.w_out_bits[tid] = __float_as_int(s_w[tid]);
+        }
+        if (args.counts_out)
+            for (int e = tid; e < E; e += NT) args.counts_out[e] = __popc(s_tok[e]);
+    }
+    if (tid == 0) s_ticket[0] = 1ull << 32 | (uint32_t)ticket;
+    lds_barrier();
+
+    // ---- jobs.  Numbers of items: n_wide items of FEW_NW wavefronts' up jobs each; then n_split up jobs that a block's
+    // wavefronts share; then ng * ncol down items.  Wide items run a block's wavefronts without a joint.  Where the
+    // up jobs are not a multiple of the grid's wavefronts, the rest of them as wide items would keep a few blocks
+    // busy (at the rate of a few CUs) while most wait for h: a rest of up to one job a block is shared out instead.
+    // (One token of the full layer: 2304 jobs on 2048 wavefronts.)
+    const int ng = 1 + n_sel, nu_s = args.inter_s / FEW_UP, nu_r = args.inter / FEW_UP, ncol = d / FEW_DN;
+    const int n_wup = nu_s + n_sel * nu_r, rest = n_wup % (FEW_NW * (int)gridDim.x);
+    const int n_split = rest <= (int)gridDim.x ? rest : 0;
+    const int n_wide = (n_wup - n_split + FEW_NW - 1) / FEW_NW, n_up = n_wide + n_split, total = n_up + ng * ncol;
+    int round = 0;                                     // of item numbers
+    // The block's item of this round: its first lane leaves it in LDS, the other wavefronts find it there.  In the up
+    // jobs wavefronts pass from round to round without waiting for each other; the barrier every 32 rounds (below)
+    // keeps the fastest from overwriting a number that the slowest has not read.
+    auto job_of_round = [&]() -> FewJob {
+        uint64_t got;
+        while ((int)((got = s_ticket[round % 64]) >> 32) != round + 1) __builtin_amdgcn_s_sleep(1);
+        const int item = __builtin_amdgcn_readfirstlane((int)got);
+        if (item >= total) return {FEW_NONE, 0, 0};    // every block comes to a number past the end
+        if (item >= n_up) return {FEW_DN_JOB, (item - n_up) / ncol, (item - n_up) % ncol};
+        const bool wide = item < n_wide;
+        const int it = wide ? item * FEW_NW + wave : n_wup - n_split + item - n_wide;
+        if (it >= n_wup) return {FEW_IDLE, 0, 0};
+        const int kind = wide ? FEW_UP_JOB : FEW_SPLIT_JOB;
+        if (it < nu_s) return {kind, 0, it * FEW_UP};
+        return {kind, 1 + (it - nu_s) / nu_r, (it - nu_s) % nu_r * FEW_UP};
+    };
     auto next_job = [&]() -> FewJob {
         round++;
         if (tid == 0) s_ticket[round % 64] = (uint64_t)(round + 1) << 32 | (uint32_t)ticket;
         return job_of_round();
     };
-    // Up items whose h is stored but not yet counted (group, or -1): vector memory operations complete in order, so
+    // Up items whose h is stored but not yet counted (the counter, or -1): vector memory operations complete in order, so
     // once a later load has been used the stores are done; before a wait for others they are waited for.
     int stored = -1;
     auto count_stored = [&](bool drain) {
@@ -455,67 +471,46 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
             st.fill(lane);
         }
         if (tid == 0) ticket = bump(arguments()->ticket);
-        FewJob then;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
         if (job.kind == FEW_IDLE) {
-            then = next_job();
+            job = next_job();
             filled = false;
-        } else if (job.kind != FEW_DN_JOB) {
-            int tok, slot, n;
-            up_rows(job, tok, slot, n);
-            const bool split = job.kind == FEW_SPLIT_JOB;
-            const int nu = stream_units_of<ST>(d), u0 = split ? split_at(nu, wave) : 0, u1 = split ? split_at(nu, wave + 1) : nu;
-            const ARows ax = {act, act_s, (uint32_t)tok * xstr + 16 * q, (uint32_t)tok * xsstr, st.wr.half};
-            int u = u0;
-            for (; u + D < u1; u += D) st.template round<true>(acc, ax, u, u1, 0, tiles[wave], lane);
-            then = next_job();
-            start(then);
-            st.template round<true>(acc, ax, u, u1, 0, tiles[wave], lane);
-            filled = then.kind != FEW_IDLE;
-            count_stored(u1 - u0 <= D);
-            if (split) {                               // the parts, joined in their order by the first wavefront
-                *(f32x4*)(tiles[wave] + lane * 16) = acc;
-                __syncthreads();
-                if (wave == 0) {
-#pragma unroll
-                    for (int w = 1; w < FEW_NW; w++) acc += *(const f32x4*)(tiles[w] + lane * 16);
-                }
-                __syncthreads();
-                if (wave) {
-                    job = then;
-                    continue;
-                }
-            }
-            // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
-            float hv[4];
-#pragma unroll
-            for (int r = 0; r < 4; r++) {
-                float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
-                if constexpr (BF) {
-                    round_bf16x2(gg, uu);
-                    hv[r] = silu_mul_fast(gg, uu);
-                } else {
-                    hv[r] = silu_mul(gg, uu);
-                }
-            }
+            continue;
+        }
+        const bool dn = job.kind == FEW_DN_JOB, split = job.kind == FEW_SPLIT_JOB;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        FewJob then;
+        int tok = 0, slot = 0, n, K = d;
+        if (dn) {
             const auto& a = *arguments();
-            if (q < 2 && r16 < n) put4<BF>(a.h + ((int64_t)(job.g ? slot : slots + slot) * a.inter_max + job.at + 4 * q) * AB, hv);
-            stored = job.g;
-        } else {
-            const auto& a = *arguments();
-            const int n = __builtin_amdgcn_readfirstlane(s_n[job.g]), K = job.g ? a.inter : a.inter_s, nu = stream_units_of<ST>(K);
+            n = __builtin_amdgcn_readfirstlane(s_n[job.g]);
+            K = job.g ? a.inter : a.inter_s;
             count_stored(true);                        // before the wait: it may be for these
-            if (tid == 0) {
+            if (wave == 0) {
                 const int need = job.g ? nu_r : nu_s;
-                while (__hip_atomic_load(&a.up_done[job.g * FEW_PAD], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < need)
+                for (;;) {
+                    const int32_t* c = &a.up_done[(job.g * FEW_SUB + lane % FEW_SUB) * FEW_PAD];
+                    int sum = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+#pragma unroll
+                    for (int o = 1; o < FEW_SUB; o *= 2) sum += __shfl_xor(sum, o, 64);
+                    if (__builtin_amdgcn_readfirstlane(sum) >= need) break;
                     __builtin_amdgcn_s_sleep(64);      // polls from every block delay the weights of those that work
-                s_last = count == ng - 1;
+                }
+                if (lane == 0) s_last = count == ng - 1;
             }
             __syncthreads();                           // also: every wavefront is past the up jobs, x is not needed any more
             combine_if_last();
-            const int ar = r16 < n ? r16 : 0;
-            for (int k0 = 0;; k0 += KC) {
+        } else {
+            up_rows(job, tok, slot, n);
+        }
+        // One loop for both kinds of job, so that its code is fetched once: a down job's h comes in chunks of KC elements,
+        // an up job's x is there.  Before the last round the stream is told what follows.
+        for (int k0 = 0, more = 1; more; k0 += KC) {
+            ARows al = {act, act_s, (uint32_t)tok * xstr + 16 * q, (uint32_t)tok * xsstr, st.wr.half};
+            const int nu = stream_units_of<ST>(K);
+            int u0 = split ? split_at(nu, wave) : 0, u1 = split ? split_at(nu, wave + 1) : nu, ua = 0;
+            if (dn) {
                 // elements [k0, k0 + kc) of the group's rows of h into LDS, as the linear takes them
+                const auto& a = *arguments();
                 const int kc = min(KC, K - k0), vecs = kc / 8;         // 8 elements a thread; a multiple of 16
                 if (k0) __syncthreads();               // the chunk before is used up
                 for (int i = tid; i < n * vecs; i += NT) {
@@ -545,19 +540,34 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
                     }
                 }
                 __syncthreads();
-                const ARows hrow = {act, act_s, (uint32_t)(ar * HSTR + 16 * q),
-                                    (uint32_t)(ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4)), ST == ST_MX4 && kc % 256 ? kc / 256 : -1};
-                const int u0 = k0 / LK, u1 = u0 + stream_units_of<ST>(kc);
-                int u = u0;
-                for (; u < u1 && u + D < nu; u += D) st.template round<true, true>(acc, hrow, u, u1, u0, tiles[wave], lane);
-                if (u < u1) {                          // the matrix's last round
+                const int ar = r16 < n ? r16 : 0;
+                al = {act, act_s, (uint32_t)(ar * HSTR + 16 * q), (uint32_t)(ar * (ST == ST_MX4 ? KC / 32 : KC / 128 * 4)),
+                      ST == ST_MX4 && kc % 256 ? kc / 256 : -1};
+                u0 = ua = k0 / LK;
+                u1 = u0 + stream_units_of<ST>(kc);
+                more = k0 + kc < K;
+            } else {
+                more = 0;
+            }
+            for (int u = u0;; u += D) {
+                const bool last = u + D >= u1;
+                if (last && !more) {
                     then = next_job();
                     start(then);
-                    st.template round<true, true>(acc, hrow, u, u1, u0, tiles[wave], lane);
-                    break;
                 }
+                if constexpr (X_LDS) {
+                    st.template round<true>(acc, al, u, u1, ua, tiles[wave], lane);
+                } else {
+                    if (dn) st.template round<true, true>(acc, al, u, u1, ua, tiles[wave], lane);
+                    else st.template round<true>(acc, al, u, u1, ua, tiles[wave], lane);
+                }
+                if (last) break;
             }
-            filled = then.kind != FEW_IDLE;
+            if (!dn) count_stored(u1 - u0 <= D);
+        }
+        filled = then.kind != FEW_IDLE;
+        const auto& a = *arguments();
+        if (dn) {
             // this lane: features 4 q .. 4 q + 3 of the group's row r16
             if (r16 < n) {
                 const int sl = s_slot[job.g][r16];
@@ -568,6 +578,34 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
             __syncthreads();
             if (tid == 0) count = bump(&a.col_done[job.at * FEW_PAD]);
             counted = job.at;
+        } else {
+            bool mine = true;                          // this wavefront has the sums
+            if (split) {                               // the parts, joined in their order by the first wavefront
+                *(f32x4*)(tiles[wave] + lane * 16) = acc;
+                lds_barrier();
+                if (wave == 0) {
+#pragma unroll
+                    for (int w = 1; w < FEW_NW; w++) acc += *(const f32x4*)(tiles[w] + lane * 16);
+                }
+                lds_barrier();
+                mine = wave == 0;
+            }
+            if (mine) {
+                // lanes of q = 0, 1 hold g and those of q = 2, 3 u of features 4 (q % 2) + r
+                float hv[4];
+#pragma unroll
+                for (int r = 0; r < 4; r++) {
+                    float gg = acc[r], uu = __shfl_xor(acc[r], 32, 64);
+                    if constexpr (BF) {
+                        round_bf16x2(gg, uu);
+                        hv[r] = silu_mul_fast(gg, uu);
+                    } else {
+                        hv[r] = silu_mul(gg, uu);
+                    }
+                }
+                if (q < 2 && r16 < n) put4<BF>(a.h + ((int64_t)(job.g ? slot : slots + slot) * a.inter_max + job.at + 4 * q) * AB, hv);
+                stored = job.g * FEW_SUB + job.at / FEW_UP % FEW_SUB;
+            }
         }
         job = then;
     }
@@ -601,7 +639,7 @@ static FewWorkspace carve_few(const moe_shape_t& s, void* base)
         off += (bytes + 255) & ~(size_t)255;
         return p;
     };
-    w.n_counters = (1 + FEW_GROUPS + (int)(d / FEW_DN)) * FEW_PAD;
+    w.n_counters = (1 + FEW_GROUPS * FEW_SUB + (int)(d / FEW_DN)) * FEW_PAD;
     w.counters = (int32_t*)take_bytes(4 * (size_t)w.n_counters);
     w.logits = (float*)take_bytes(4 * T * (size_t)s.E);
     if (s.w_dtype == MOE_FP8_E4M3 || s.w_dtype == MOE_MXFP4) {
@@ -680,7 +718,7 @@ hipError_t launch_few(const moe_shape_t& s, const void* x, const float* Wg, cons
     a.counts_out = counts_out;
     a.ticket = w.counters;
     a.up_done = w.counters + FEW_PAD;
-    a.col_done = w.counters + (1 + FEW_GROUPS) * FEW_PAD;
+    a.col_done = w.counters + (1 + FEW_GROUPS * FEW_SUB) * FEW_PAD;
     if (s.act_dtype == MOE_F32) return launch_few_t<ST_F32>(s, x, Wg, bias, a, w, stream);
     if (s.w_dtype == MOE_FP8_E4M3) return launch_few_t<ST_FP8>(s, x, Wg, bias, a, w, stream);
     if (s.w_dtype == MOE_MXFP4) return launch_few_t<ST_MX4>(s, x, Wg, bias, a, w, stream);
