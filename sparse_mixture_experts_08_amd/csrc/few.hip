@@ -240,7 +240,9 @@ template <int ST, bool X_LDS>
 __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
 {
     constexpr bool BF = ST != ST_F32;                  // activations are bf16
-    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = 8;
+    // D weight units in flight a wavefront.  Where x travels along from memory, eight of both spill (16 bf16 tokens of a
+    // 64-expert layer 1178 us, 737 with four; 8 fp32 tokens 532 and 412); where it lies in LDS eight fit.
+    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = X_LDS ? 8 : 4;
     constexpr int XB = FewAct<ST>::bytes, HSTR = FEW_ROW + 16;
     constexpr int KC = FEW_ROW / XB / (LK * D) * (LK * D);             // elements of h in LDS at a time: whole rounds
     static_assert(KC > 0, "a round of h fits a row");
