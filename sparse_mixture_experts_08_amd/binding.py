@@ -3,6 +3,7 @@
 Every step of the layer runs in the library's HIP kernels; torch supplies device memory and the current
 stream.  Importing works without a GPU; calling a function without the built library raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -114,7 +115,16 @@ def _ptr(t):
 
 
 def _stream(dev):
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if dev.type != "cuda":
+        raise ValueError(f"Expected a cuda device, but got: {dev}")
+    # the handle alone: a torch.cuda.Stream object costs 2 us, a sixth of a small call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(dev.index))
+
+
+def _on(dev):
+    """A context in which `dev` is the current device (kernels are launched there)."""
+    here = dev.type == "cuda" and dev.index == torch.cuda.current_device()
+    return contextlib.nullcontext() if here else torch.cuda.device(dev)
 
 
 def _workspace(shape, dev, workspace):
@@ -187,7 +197,7 @@ def moe_quantize_mx(x, fmt):
     rows, cols = x.shape
     q = torch.empty((rows, cols // 2 if fmt == MOE_MXFP4 else cols), dtype=torch.uint8, device=x.device)
     s = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
-    with torch.cuda.device(x.device):
+    with _on(x.device):
         st = lib().moe_quantize_mx(rows, cols, _ptr(x), _act_code(x), fmt, _ptr(q), _ptr(s), _stream(x.device))
     if st:
         raise MoeError(st, "moe_quantize_mx")
@@ -206,7 +216,7 @@ def moe_dequantize_mx(q, scales, fmt, dtype=torch.bfloat16):
     if dtype not in (torch.bfloat16, torch.float32):
         raise ValueError("dtype must be bf16 or fp32")
     out = torch.empty((rows, cols), dtype=dtype, device=q.device)
-    with torch.cuda.device(q.device):
+    with _on(q.device):
         st = lib().moe_dequantize_mx(rows, cols, _ptr(q), _ptr(scales), fmt, _act_code(out), _ptr(out), _stream(q.device))
     if st:
         raise MoeError(st, "moe_dequantize_mx")
@@ -310,7 +320,7 @@ def moe_forward_routed(x, idx, w, W1, W3, W2, S1, S3, S2, scales=None, y=None, w
     shape, sc, y = _layer(x, k, E, W1, W3, W2, S1, S3, S2, scales, y,
                           [("idx", idx, torch.int32, (x.shape[0], k)), ("w", w, torch.float32, (x.shape[0], k))])
     dev = x.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         workspace, need = _workspace(shape, dev, workspace)
         c = torch.empty(E, dtype=torch.int32, device=dev) if counts else None
         if counts and x.shape[0] == 0:
@@ -336,7 +346,7 @@ def moe_forward_few(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=None,
     shape, sc, y = _layer(x, k, E, W1, W3, W2, S1, S3, S2, scales, y,
                           [("Wg", Wg, torch.float32, (E, d)), ("bias", bias, torch.float32, (E,))])
     dev = x.device
-    with torch.cuda.device(dev):
+    with _on(dev):
         if workspace is None:
             need = moe_few_workspace_size(shape)
             if need == 0:
@@ -374,7 +384,7 @@ def moe_forward_noalloc(x, Wg, bias, W1, W3, W2, S1, S3, S2, k, scales=None, y=N
         r = dict(idx=torch.empty((T, k), dtype=torch.int32, device=dev),
                  w=torch.empty((T, k), dtype=torch.float32, device=dev),
                  counts=torch.empty(E, dtype=torch.int32, device=dev))
-    with torch.cuda.device(dev):      # the library uses the current device's scratch array
+    with _on(dev):      # the library uses the current device's scratch array
         st = lib().moe_forward_noalloc(ctypes.byref(shape), _ptr(x), _ptr(Wg), _ptr(bias), _ptr(W1), _ptr(W3),
                                        _ptr(W2), _ptr(sc.get("W1s")), _ptr(sc.get("W3s")), _ptr(sc.get("W2s")),
                                        _ptr(S1), _ptr(S3), _ptr(S2), _ptr(sc.get("S1s")), _ptr(sc.get("S3s")),

@@ -222,9 +222,9 @@ template <> struct FewAct<ST_BF16> { static constexpr int bytes = 2; };
 template <> struct FewAct<ST_FP8> { static constexpr int bytes = 1; };
 template <> struct FewAct<ST_MX4> { static constexpr int bytes = 1; };
 
-// LDS for activations: 16 rows of up to 7168 bytes, each padded by 16 so that 16 rows' pieces fall on distinct banks.
+// LDS for activations: 16 rows of up to 7168 bytes, each padded so that 16 rows' pieces fall on distinct banks.
 // X_LDS: x fits (rows of d elements) and is kept there for the up items.
-constexpr int FEW_ROW = 7168, FEW_XBYTES = 16 * (FEW_ROW + 16), FEW_XSCALES = 16 * FEW_ROW / 32;
+constexpr int FEW_ROW = 7168, FEW_XBYTES = 16 * (FEW_ROW + STREAM_PAD), FEW_XSCALES = 16 * FEW_ROW / 32;
 
 // First unit of wavefront w's part of nu units, at a multiple of four (a scale load's units).
 __device__ __forceinline__ int split_at(int nu, int w) { return min(nu, (nu + 3) / 4 * w / FEW_NW * 4); }
@@ -243,7 +243,7 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     // D weight units in flight a wavefront.  Where x travels along from memory, eight of both spill (16 bf16 tokens of a
     // 64-expert layer 1178 us, 737 with four; 8 fp32 tokens 532 and 412); where it lies in LDS eight fit.
     constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = X_LDS ? 8 : 4;
-    constexpr int XB = FewAct<ST>::bytes, HSTR = FEW_ROW + 16;
+    constexpr int XB = FewAct<ST>::bytes, HSTR = FEW_ROW + STREAM_PAD;
     constexpr int KC = FEW_ROW / XB / (LK * D) * (LK * D);             // elements of h in LDS at a time: whole rounds
     static_assert(KC > 0, "a round of h fits a row");
     __shared__ __attribute__((aligned(16))) uint8_t act[FEW_XBYTES];   // x; then h
@@ -263,7 +263,7 @@ __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int r16 = lane & 15, q = lane >> 4;
     const int T = args.T, k = args.k, E = args.E, d = args.d, slots = T * k;
-    const int xstr = d * XB + (X_LDS ? 16 : 0);        // bytes between rows of x
+    const int xstr = d * XB + (X_LDS ? STREAM_PAD : 0); // bytes between rows of x
     const int xsstr = ST == ST_MX4 ? d / 32 : ST == ST_FP8 ? d / 128 * 4 : 0;   // ... of its scales
     int ticket = 0;
     if (tid == 0) ticket = bump(args.ticket);
@@ -678,7 +678,7 @@ static hipError_t launch_few_t(const moe_shape_t& s, const void* x, const float*
     hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
     // a block for each of the card's 256 CUs (any number is right: see above)
-    const int64_t row = s.d * FewAct<ST>::bytes + 16;  // of x in LDS
+    const int64_t row = s.d * FewAct<ST>::bytes + STREAM_PAD;  // of x in LDS
     if (s.T * row <= FEW_XBYTES && s.T * s.d / 32 <= FEW_XSCALES) few_layer_kernel<ST, true><<<256, 64 * FEW_NW, 0, stream>>>(a);
     else few_layer_kernel<ST, false><<<256, 64 * FEW_NW, 0, stream>>>(a);
     return hipGetLastError();

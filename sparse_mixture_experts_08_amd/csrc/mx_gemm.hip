@@ -42,7 +42,7 @@ template <bool UP>
 __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
 {
     constexpr int NW = 16, NT = 64 * NW, FW = UP ? 8 : 16, BN = NW * FW, D = 4;
-    constexpr int XK = UP ? 7168 : 4096, XSTR = XK + 16;               // whole rounds of D units
+    constexpr int XK = UP ? 7168 : 4096, XSTR = XK + STREAM_PAD;       // whole rounds of D units
     static_assert(XK % (D * 256) == 0, "a chunk of K is whole rounds");
     __shared__ __attribute__((aligned(16))) uint8_t xb[16 * XSTR];
     __shared__ __attribute__((aligned(16))) uint8_t xs[16 * (XK / 32)];

@@ -36,6 +36,7 @@ template <> struct StreamType<ST_FP8> { static constexpr int K = 128, NA = 2; };
 template <> struct StreamType<ST_MX4> { static constexpr int K = 256, NA = 4; };
 
 constexpr int STREAM_TILE = 16 * 128;                  // LDS bytes of one unit
+constexpr int STREAM_PAD = 32;                         // behind a row of activations in LDS: see WUnit::put
 
 template <int ST> __device__ __forceinline__ int stream_units_of(int K)
 {
@@ -78,18 +79,19 @@ template <int ST> struct WUnit {
         p[0] = __builtin_nontemporal_load((const i32x4*)(r.p0 + (int64_t)u * 128 + o));
         p[1] = __builtin_nontemporal_load((const i32x4*)(r.p1 + (int64_t)u * 128 + o));
     }
-    // Into the wavefront's tile: chunk c of row r at chunk c ^ f(r), f(r) = (r ^ (r >> 3 & 1)) & 7, so that the 16
-    // rows of a read fall on distinct banks.
+    // Into the wavefront's tile: chunk c of row r at chunk c ^ (r / 2 % 8).  A 16-byte read takes 16 lanes a clock: lanes
+    // 0-3, 12-15 and 20-27, then 4-11, 16-19 and 28-31, and so on, that is half of the 16 rows at one chunk and the
+    // other half at the next, which this places on all 64 banks.
     __device__ __forceinline__ void put(uint8_t* tile, int lane) const
     {
         const int row = lane >> 3, c = lane & 7;
-        *(i32x4*)(tile + row * 128 + ((c ^ row) << 4)) = p[0];
-        *(i32x4*)(tile + (row + 8) * 128 + ((c ^ (row ^ 1)) << 4)) = p[1];
+        *(i32x4*)(tile + row * 128 + ((c ^ row >> 1) << 4)) = p[0];
+        *(i32x4*)(tile + (row + 8) * 128 + ((c ^ (row >> 1 ^ 4)) << 4)) = p[1];
     }
     // The pieces of row l % 16 as an MFMA operand takes them: chunks q and 4 + q.
     static __device__ __forceinline__ void get(const uint8_t* tile, int lane, i32x4 (&v)[2])
     {
-        const int row = lane & 15, q = lane >> 4, f = (row ^ (row >> 3)) & 7;
+        const int row = lane & 15, q = lane >> 4, f = row >> 1;
         v[0] = *(const i32x4*)(tile + row * 128 + ((q ^ f) << 4));
         v[1] = *(const i32x4*)(tile + row * 128 + (((4 + q) ^ f) << 4));
     }

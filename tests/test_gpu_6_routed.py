@@ -91,6 +91,24 @@ def test_parity(wt, shape):
     close(y, reference(inp, idx, w, wt), wt)
 
 
+@pytest.mark.parametrize("d,inter,inter_s", [(128, 128, 128), (640, 384, 256), (1152, 256, 128), (1536, 512, 256)])
+def test_mxfp4_tiles_of_every_height(d, inter, inter_s):
+    # tiles of each number of 64-row steps, full, one row short and one row over; reductions of one stage of 128, of
+    # fewer and more than the ring holds, with scale rows in whole 16-byte words and without
+    say(f"[routed] tile heights d={d} inter={inter}")
+    rows = [0, 1, 16, 17, 63, 64, 65, 127, 128, 129, 192, 193, 255, 256, 257, 513]
+    T, E = sum(rows), len(rows)
+    inp = make("mxfp4", T, d, E, 1, inter, inter_s)
+    g = torch.Generator().manual_seed(11)
+    idx = torch.repeat_interleave(torch.arange(E), torch.tensor(rows))[torch.randperm(T, generator=g)].to(torch.int32).view(T, 1)
+    w = torch.rand((T, 1), generator=g) + 0.5
+    y, counts = routed(inp, idx, w, counts=True)
+    assert counts.tolist() == rows
+    close(y, reference(inp, idx, w, "mxfp4"), "mxfp4")
+    again, _ = routed(inp, idx, w, counts=True)
+    assert torch.equal(bits(y), bits(again))
+
+
 @pytest.mark.parametrize("wt", ["mxfp4", "bf16"])
 @pytest.mark.parametrize("T,E,k", [(40, 16, 4), (300, 16, 4), (300, 16, 5), (1, 8, 3)])
 def test_slots_without_an_expert(wt, T, E, k):
