@@ -227,11 +227,6 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
                 dma4(baseS + (int64_t)min(4 * c + j, nstages - 1) * 4, offS, scl0 + j * 2048 + wave * 256);
     };
 
-    f32x4 acc[WM][WB];                                 // UP: features of W1, then of W3
-#pragma unroll
-    for (int i = 0; i < WM; i++)
-#pragma unroll
-        for (int j = 0; j < WB; j++) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
     // Fragments in a stage: the row blocks of a wavefront are multiples of 16 rows apart, and the orders repeat
     // every 16 rows.
     const int a_lo = mx_swz128(16 * mg + r16, q), a_hi = mx_swz128(16 * mg + r16, 4 + q);
@@ -245,6 +240,11 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
             constexpr int STAGE = NR * 8192 + NB * 64, FIT = MX_RING / STAGE, NSTG = FIT < 6 ? FIT : 6;
             constexpr int NL = NR + PB;                // loads per wavefront and stage
             static_assert(NSTG >= 3 && (NSTG - 2) * NL < 64, "two stages ahead; vmcnt range");
+            f32x4 acc[NR][WB];                                 // UP: features of W1, then of W3
+#pragma unroll
+            for (int i = 0; i < NR; i++)
+#pragma unroll
+                for (int j = 0; j < WB; j++) acc[i][j] = (f32x4){0.f, 0.f, 0.f, 0.f};
             const bool last = 16 * (4 * (NR - 1) + mg) < rows;         // the last step's block has rows (wave-uniform)
             auto issue = [&](int buf, int s) {
                 const uint32_t dst = ring0 + buf * STAGE + wave * 1024;
@@ -335,54 +335,56 @@ __global__ __launch_bounds__(512, 2) void mx_gemm_kernel(GemmArgs g)
                 if (s + 3 < nstages) stage(IntC<3>{}, s + 3, buf);
             }
             if (!late) lds_barrier();
+            wait_vmcnt<0>();                           // no load may still target this block's LDS
+            lds_barrier();
+            // the output tile into LDS, of the steps that the tile has
+            if constexpr (UP) {
+                // h of a token's 32 features lies on the four lanes r16 + 16 q, eight values each
+#pragma unroll
+                for (int i = 0; i < NR; i++) {
+                    const int row = 16 * (4 * i + mg) + r16;
+#pragma unroll
+                    for (int p = 0; p < WN / 2; p++) {
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            float gg = acc[i][2 * p + e / 4][e % 4], uu = acc[i][WN + 2 * p + e / 4][e % 4];
+                            round_bf16x2(gg, uu);
+                            v[e] = round_bf16(silu_mul_fast(gg, uu));
+                        }
+                        uint32_t am = mx_amax8(v);
+                        am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
+                        am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
+                        const uint32_t c = mx_scale_code<false>(am);
+                        const uint2 pk = c == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(v, c);
+                        const int f = ng * 64 + p * 32;
+                        *(uint32_t*)(ring + row * OSTR + f + 4 * q) = pk.x;
+                        *(uint32_t*)(ring + row * OSTR + f + 16 + 4 * q) = pk.y;
+                        if (q == 0 && row < rows) ((uint8_t*)g.outs)[((int64_t)row0 + row) * g.ldos + (n0 + f) / 32] = (uint8_t)c;
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < NR; i++) {
+#pragma unroll
+                    for (int j = 0; j < WB; j++) {
+                        const uint32_t lo = f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]);
+                        const uint32_t hi = f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]);
+                        *(uint2*)(ring + (16 * (4 * i + mg) + r16) * OSTR + (ng * (BN / 2) + j * 16 + 4 * q) * 2) = make_uint2(lo, hi);
+                    }
+                }
+            }
         }
     };
     with_count<WM>(__builtin_amdgcn_readfirstlane((rows + 63) / 64), k_walk);
-    wait_vmcnt<0>();                                   // no load may still target this block's LDS
-    lds_barrier();
-
+    __syncthreads();
     if constexpr (UP) {
-        // h of a token's 32 features lies on the four lanes r16 + 16 q, eight values each
-#pragma unroll
-        for (int i = 0; i < WM; i++) {
-            const int row = 16 * (4 * i + mg) + r16;
-#pragma unroll
-            for (int p = 0; p < WN / 2; p++) {
-                float v[8];
-#pragma unroll
-                for (int e = 0; e < 8; e++) {
-                    float gg = acc[i][2 * p + e / 4][e % 4], uu = acc[i][WN + 2 * p + e / 4][e % 4];
-                    round_bf16x2(gg, uu);
-                    v[e] = round_bf16(silu_mul_fast(gg, uu));
-                }
-                uint32_t am = mx_amax8(v);
-                am = max(am, (uint32_t)__shfl_xor((int)am, 16, 64));
-                am = max(am, (uint32_t)__shfl_xor((int)am, 32, 64));
-                const uint32_t c = mx_scale_code<false>(am);
-                const uint2 pk = c == 255u ? make_uint2(0u, 0u) : mx_pack_fp8(v, c);
-                const int f = ng * 64 + p * 32;
-                *(uint32_t*)(ring + row * OSTR + f + 4 * q) = pk.x;
-                *(uint32_t*)(ring + row * OSTR + f + 16 + 4 * q) = pk.y;
-                if (q == 0 && row < rows) ((uint8_t*)g.outs)[((int64_t)row0 + row) * g.ldos + (n0 + f) / 32] = (uint8_t)c;
-            }
-        }
-        __syncthreads();
         constexpr int CH = BN / 16;
-        for (int idx = tid; idx < BM * CH; idx += 512) {
+        for (int idx = tid; idx < rows * CH; idx += 512) {
             const int row = idx / CH, ch = idx % CH;
-            if (row < rows)
-                *(uint4*)(g.out + ((int64_t)row0 + row) * g.ldo + n0 + ch * 16) = *(const uint4*)(ring + row * OSTR + ch * 16);
+            *(uint4*)(g.out + ((int64_t)row0 + row) * g.ldo + n0 + ch * 16) = *(const uint4*)(ring + row * OSTR + ch * 16);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < WM; i++)
-#pragma unroll
-            for (int j = 0; j < WB; j++) {
-                const uint32_t lo = f32x2_to_bf16x2(acc[i][j][0], acc[i][j][1]);
-                const uint32_t hi = f32x2_to_bf16x2(acc[i][j][2], acc[i][j][3]);
-                *(uint2*)(ring + (16 * (4 * i + mg) + r16) * OSTR + (ng * (BN / 2) + j * 16 + 4 * q) * 2) = make_uint2(lo, hi);
-            }
-        __syncthreads();
         store_tile_bf16<BM, BN, OSTR, 512, true>(ring, g.out, g.ldo, row0, rows, n0);
     }
 }
