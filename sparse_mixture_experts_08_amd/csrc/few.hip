@@ -12,6 +12,10 @@
 //     output features a wavefront.  A down item waits for its expert's up items, its first weights on their way
 //     meanwhile, and the block that completes the last down item of a column range sums the experts' outputs there.
 //     No launch boundary lies between the phases.
+// Full layer: one token 61 us in MXFP4 (218 MB; 31 us at the 7.1 TB/s of a read alone), 139 us in bf16 (800 MB; 113), four
+// tokens in fp8 226 us (1.4 GB; 197), sixteen in MXFP4 156 us (1.1 GB; 160, these few experts partly cached); launch 1
+// another 5 to 9 us.  What is lost at one token: the selection (6 us), the wait for the slowest block's h
+// and the down jobs' two rounds.
 //
 // Why every wait ends.  Blocks take item numbers from the counter in ascending order, and an item waits only for
 // items of lower numbers.  Take the lowest unfinished item: the block that holds it is running (it took the

@@ -37,6 +37,8 @@ template <bool UP> __device__ __forceinline__ MxGroup mx_group(const GemmArgs& g
 // 16-row tiles (decode): weight bytes bound it.  A block is one tile x 256 output features for the down GEMM, 128
 // for the up GEMM; each of its 16 wavefronts streams 16 weight rows (up: eight of W1 and the same eight of W3) over
 // the whole K, the tile's activation rows in LDS (up to XK elements of K at a time).
+// 64 tokens of the full layer (222 experts, 5.2 GB): up 565 us, down 295 us, 6.1 TB/s.  With loads in operand order (16
+// rows x 64 bytes an instruction) and the activations from memory it was 1228 and 611 us.
 // ---------------------------------------------------------------------------------------------------
 template <bool UP>
 __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
@@ -145,7 +147,12 @@ __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
 //
 // Eight wavefronts, 4 (rows) x 2 (features), two to a SIMD, which take turns: while one reads the fragments of a
 // stage into registers, the other one multiplies.  Barriers separate the turns, wavefronts 4-7 being one turn
-// behind.  Row blocks (16 rows) are dealt to the row groups in turn, so a short tile still spreads over all.
+// behind (in step with each other, all reading, then all multiplying: up GEMM of 16384 tokens 4.93 against 3.80 ms).
+// Row blocks (16 rows) are dealt to the row groups in turn, so a short tile still spreads over all.
+//
+// Full layer, 4096 tokens (144 rows a tile): up 1232 us, down 681 us; 16384 skewed tokens: 3707 and 1958 us, 2.3 PFLOP/s.
+// A stage's loads (48 KB a CU for 256 rows, mostly from L2) take about as long as its products; the
+// 4096-token up GEMM takes 944 us without loads in the loop, and 1100 us with loads alone.
 // ---------------------------------------------------------------------------------------------------
 constexpr int MX_BM = 256, MX_RING = 3 * (MX_BM * 128 + 256 * 64);
 
