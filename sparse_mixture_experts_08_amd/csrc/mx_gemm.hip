@@ -152,7 +152,7 @@ __global__ __launch_bounds__(1024, 4) void mx_gemm_stream_kernel(GemmArgs g)
 //
 // Full layer, 4096 tokens (144 rows a tile): up 1232 us, down 681 us; 16384 skewed tokens: 3707 and 1958 us, 2.3 PFLOP/s.
 // A stage's loads (48 KB a CU for 256 rows, mostly from L2) take about as long as its products; the
-// 4096-token up GEMM takes 944 us without loads in the loop, and 1100 us with loads alone.
+// 4096-token up GEMM takes 944 us without loads in the loop, and about 1160 us with loads alone.
 // ---------------------------------------------------------------------------------------------------
 constexpr int MX_BM = 256, MX_RING = 3 * (MX_BM * 128 + 256 * 64);
 

@@ -70,7 +70,7 @@ SHAPES = [  # T, d, E, k, inter, inter_shared
     (5, 384, 300, 16, 128, 384),             # E > 256, k = 16, d an odd multiple of 128
     (63, 1024, 64, 6, 384, 256),             # 16-row tiles; the one-block permutation
     (257, 256, 1024, 8, 128, 128),           # the chunked permutation, many empty experts
-    (600, 512, 16, 4, 256, 384),             # 128-row tiles (bf16: 256)
+    (600, 512, 16, 4, 256, 384),             # 128-row tiles (bf16, MXFP4: 256)
     (600, 384, 16, 4, 384, 256),             # ... with an odd d and inter
     (1100, 512, 8, 2, 256, 384),             # 256-row tiles
     (500, 128, 4, 2, 128, 256),
@@ -137,6 +137,23 @@ def test_no_slot_has_an_expert(wt, T):
     y, counts = routed(inp, idx, w, counts=True)
     assert int(counts.abs().sum()) == 0
     close(y, reference(inp, idx, torch.zeros_like(w), wt), wt)
+
+
+@pytest.mark.parametrize("wt", ["mxfp4", "fp8", "bf16", "f32"])
+@pytest.mark.parametrize("T", [40, 300])
+def test_a_token_that_is_not_finite_stays_alone(wt, T):
+    # every column of its rows is lost, and no bit of another token's
+    say(f"[routed] NaN and infinity {wt} T={T}")
+    inp = make(wt, T, 384, 6, 3, 256, 128)
+    idx, w = routing(T, 6, 3)
+    y = routed(inp, idx, w)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[[3, T - 1]] = True
+    inp["x"][3, 17] = float("nan")
+    inp["x"][T - 1, 200] = float("inf")
+    z = routed(inp, idx, w)
+    assert not torch.isfinite(z[bad.to(DEV)].float()).any()
+    assert torch.equal(bits(z[~bad.to(DEV)]), bits(y[~bad.to(DEV)]))
 
 
 @pytest.mark.parametrize("wt", ["mxfp4", "fp8", "f32"])
