@@ -17,9 +17,12 @@ int tile_rows(const moe_shape_t& s)
     // streaming).  Otherwise bf16 takes 256-row tiles: an expert of up to 256 rows reads its weights once,
     // and a 256 x 256 output block needs fewer staged bytes per MFMA than 128 x 512; row blocks past a
     // tile's end are skipped.  fp8 takes 256-row tiles above 192 rows per expert (fewer staged bytes and
-    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.  MXFP4: 256, its kernel stages only the rows a
-    // tile has.
+    // LDS fragment reads per MFMA), else 128; fp32 keeps 128.  MXFP4: 16-row tiles
+    // to 11 rows, else 256, of which its kernel stages only the rows there (d 7168, inter 2048, us with 16 / 256: 64 experts,
+    // 8 rows each 304 / 369, 12 329 / 379, 16 431 / 386, 24 589 / 418; 256 experts, 10 each 1169 / 1328, 12 each
+    // but skewed 1009 / 501: a hot expert's 16-row tiles read its weights once each).
     const int64_t per_expert = s.T * s.k / (s.E > 0 ? s.E : 1);
+    if (s.w_dtype == MOE_MXFP4) return per_expert <= 11 ? 16 : 256;
     if (per_expert <= 24) return 16;
     if (s.w_dtype == MOE_FP8_E4M3) return per_expert > 192 ? 256 : 128;
     if (s.act_dtype == MOE_F32) return 128;
