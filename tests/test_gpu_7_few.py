@@ -86,6 +86,14 @@ def test_full_width_rows(wt):
     check(make(wt, 4, 7168, 12, 8, 2048, 2048), 8, wt)
 
 
+@pytest.mark.parametrize("wt,T,d", [("f32", 16, 2048), ("f32", 5, 7168), ("bf16", 9, 7168), ("bf16", 16, 3712),
+                                    ("fp8", 16, 7296), ("mxfp4", 16, 7296)])
+def test_x_longer_than_the_lds(wt, T, d):
+    # the up products then take x from memory with the weights; 7296 is an odd multiple of 128
+    say(f"[few] x from memory {wt} T={T} d={d}")
+    check(make(wt, T, d, 10, 3, 256, 384, skew=True), 3, wt)
+
+
 def test_ties_go_to_the_lower_expert():
     say("[few] ties")
     inp = make("bf16", 16, 512, 64, 6, 128, 128)
