@@ -244,9 +244,10 @@ template <int ST, bool X_LDS>
 __global__ __launch_bounds__(64 * FEW_NW, 2) void few_layer_kernel(FewArgs args)
 {
     constexpr bool BF = ST != ST_F32;                  // activations are bf16
-    // D weight units in flight a wavefront.  Where x travels along from memory, eight of both spill (16 bf16 tokens of a
-    // 64-expert layer 1178 us, 737 with four; 8 fp32 tokens 532 and 412); where it lies in LDS eight fit.
-    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = X_LDS ? 8 : 4;
+    // D weight units in flight a wavefront: eight where x lies in LDS.  Where x travels along from memory, as many as
+    // do not spill: four (16 bf16 tokens of a 64-expert layer 737 us, 1178 with eight; 8 fp32 tokens 412 and 532), in
+    // MXFP4, whose units hold the most of x, two (16 tokens of d = 7296, 64 experts 408 us, 612 with four).
+    constexpr int AB = BF ? 2 : 4, NT = 64 * FEW_NW, LK = StreamType<ST>::K, D = X_LDS ? 8 : ST == ST_MX4 ? 2 : 4;
     constexpr int XB = FewAct<ST>::bytes, HSTR = FEW_ROW + STREAM_PAD;
     constexpr int KC = FEW_ROW / XB / (LK * D) * (LK * D);             // elements of h in LDS at a time: whole rounds
     static_assert(KC > 0, "a round of h fits a row");
